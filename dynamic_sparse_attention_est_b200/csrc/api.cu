@@ -479,6 +479,11 @@ int do_static_attention(int pattern, const Common &c, const void *q, const void 
 
 }  // namespace
 
+int api_fail(int code, const char *msg) { return fail(code, "%s", msg); }
+int api_select_device(const void *ptr) { return select_device(ptr); }
+int api_check_ws(void *ws, size_t ws_bytes, size_t need) { return check_ws(ws, ws_bytes, need); }
+unsigned long long api_wait_limit_ns() { return g_wait_limit_ns.load(); }
+
 // The driver's tensor-map encoder, looked up once.
 PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
     std::call_once(g_encode_once, [] {
@@ -854,9 +859,15 @@ int minf_status(void *ws, minf_stream_t stream) {
     int st[2] = {0, 0};
     e = cudaMemcpy(st, ws, sizeof(st), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy status");
-    if (st[0] != 0) {
+    if (st[0] == MINF_ERR_INVALID) {
+        static const char *const what[] = {"data", "sequence lengths", "page number", "position", "page list"};
+        const int i = st[1] & 0xff;
+        fail(st[0], "device check found a bad %s in the call's arrays; its part was left out", what[i < 5 ? i : 0]);
+    } else if (st[0] != 0) {
         fail(st[0], "device wait gave up at site 0x%08x (role %d, barrier %d, tile %d)", st[1],
              (st[1] >> 24) & 0x3f, (st[1] >> 16) & 0xff, st[1] & 0xffff);
+    }
+    if (st[0] != 0) {
         e = cudaMemset(ws, 0, sizeof(st));
         if (e != cudaSuccess) return cuda_fail(e, "cudaMemset status");
     }

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -9,6 +10,13 @@
 namespace minf {
 
 struct AttnParams;
+
+// Host helpers of the entry points (api.cu): an error code with its message, the
+// device of a pointer made current, a workspace checked, the wait limit.
+int api_fail(int code, const char *msg);
+int api_select_device(const void *ptr);
+int api_check_ws(void *ws, size_t ws_bytes, size_t need);
+unsigned long long api_wait_limit_ns();
 
 // Launch timing (minf_profile_enable): while enabled, an event pair around the
 // scope's launches on `st`, read back by minf_profile_read.
@@ -42,6 +50,8 @@ struct VsPlanBufs {
     float *diag_o;              // [n_heads][n][128] its unnormalised O
 };
 
+// The driver's tensor-map encoder (null if it cannot be found).
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder();
 // 3D TMA map over a bf16 [heads][n][128] tensor: box {64, 64, 1}, 128B swizzle.
 cudaError_t make_tmap_3d(CUtensorMap *map, const void *base, int heads, int n);
 cudaError_t make_tmap_f32_3d(CUtensorMap *map, const void *base, int x, int y, int z);

@@ -1,0 +1,658 @@
+// paged_stream.cu -- attention of few query rows over many stored keys: decoding
+// steps over everything stored, and every token over its own selected pages.
+//
+// A work item is one kv-head of one sequence (dense) or token (selected pages)
+// with up to 8 NT of its query rows (tokens x the group's q-heads).  Its K and V
+// are read once and used for a handful of rows, so the time is that of reading
+// them: HBM when each key belongs to one item, L2 when the tokens of a chunk
+// share their pages.  The kernel is built around the loads.
+//
+//   * Warps take 16-key groups and keep a softmax state of their own; nothing
+//     synchronises until the end of an item.  K goes from global memory to the
+//     registers of the matrix instruction without shared memory in between: the
+//     product S^T = K Q^T contracts over channels, in any order that K and Q
+//     share, so a lane's 16 contiguous bytes serve as its fragments.  V^T P^T
+//     contracts over keys; a lane loads 16 bytes of four keys' rows and pairs
+//     them with byte permutes.  The loads of the next group's K and of this
+//     group's V are in flight while this group is computed.
+//   * With keys on the 16-row side and query rows on the 8-column side
+//     (m16n8k16), four or eight q-heads of a group fill the tile, where a
+//     128-row tensor-memory tile would compute 16 to 32 rows for each one used.
+//   * Running maximum and sum per row in fp32, log2 domain; the maximum moves
+//     only past a margin, which one vote per group decides.
+//   * Dense items are cut at equal shares of all 16-key groups of the call (each
+//     CTA takes the prefix sums of the lengths itself, so that a captured launch
+//     follows them), however uneven the lengths; an item's parts are joined by a
+//     second small kernel in a fixed order.
+#include "internal.h"
+#include "paged.cuh"
+
+namespace minf {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kGroup = 16;         // keys per warp step
+constexpr int kStreamGrid = 592;   // 148 SMs x 4
+constexpr int kOPad = 132;         // floats per row of the CTA's join buffer
+
+__device__ __forceinline__ uint4 ldg_stream(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
+
+// 8x8 transpose of 16-bit elements over a warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// The pages a warp walks: 32 (logical block, page) entries at a time, one per
+// lane, the next 32 already loaded.
+template <bool kSparse>
+struct PageWalk {
+    const PagedSeqs *S;
+    WsHeader *hdr;
+    const int *list;  // selected blocks (sparse)
+    int seq, n_slots, last_blk, base;
+    int blk, pg, blk_next, pg_next;
+
+    __device__ __forceinline__ void fetch(int slot, int &b, int &p) const {
+        b = p = -1;
+        if (slot >= n_slots) return;
+        if (kSparse) {
+            b = __ldg(list + slot);
+            // an entry that is negative, past the query's own page or not above the one before it is left out
+            if (b < 0 || b > last_blk || (slot > 0 && b <= __ldg(list + slot - 1))) {
+                b = -1;
+                return;
+            }
+        } else {
+            b = slot;
+        }
+        p = page_of(*S, seq, b, hdr);
+    }
+    __device__ __forceinline__ void start(int slot, int lane) {
+        base = slot;
+        fetch(base + lane, blk, pg);
+        fetch(base + 32 + lane, blk_next, pg_next);
+    }
+    // Entry `slot`, not before the one asked for last; the whole warp calls it.
+    __device__ __forceinline__ void get(int slot, int lane, int &b, int &p) {
+        while (slot >= base + 32) {
+            base += 32;
+            blk = blk_next;
+            pg = pg_next;
+            fetch(base + 32 + lane, blk_next, pg_next);
+        }
+        b = __shfl_sync(0xffffffffu, blk, slot - base);
+        p = __shfl_sync(0xffffffffu, pg, slot - base);
+    }
+};
+
+struct Item {
+    int seq, h, row0, rows;  // rows row0 .. row0 + rows - 1 of the (token, q-head of the group) list
+    int tok0;                // q row of the sequence's first token (sparse: of the token)
+    int pos0;                // position of that token
+    int len;                 // stored tokens
+};
+
+template <class Ty, int NT>
+struct State {
+    float m[NT][2], l[NT][2];
+    float o[NT][8][4];
+};
+
+// One 16-key group: scores, softmax, P V.
+template <class Ty, int NT>
+__device__ __forceinline__ void step(State<Ty, NT> &st, const uint4 (&kr)[8], const uint4 (&vr)[8],
+                                     const uint4 (&qf)[NT][4], int key0, const int (&lim)[NT][2], int min_lim,
+                                     float sl2, int lane) {
+    const int r = lane >> 2;
+    float s[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            // kr[i]: key r, channels 8 (c + 4 i) ..; kr[4 + i]: key r + 8
+            Ty::mma(s[t], kr[i].x, kr[4 + i].x, kr[i].y, kr[4 + i].y, qf[t][i].x, qf[t][i].y);
+            Ty::mma(s[t], kr[i].z, kr[4 + i].z, kr[i].w, kr[4 + i].w, qf[t][i].z, qf[t][i].w);
+        }
+    if (key0 + kGroup > min_lim) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (key0 + r >= lim[t][i]) s[t][i] = -INFINITY;
+                if (key0 + r + 8 >= lim[t][i]) s[t][2 + i] = -INFINITY;
+            }
+    }
+    bool grow = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) grow |= fmaxf(s[t][i], s[t][2 + i]) * sl2 > st.m[t][i] + Ty::kLag;
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x = fmaxf(s[t][i], s[t][2 + i]);
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * sl2;
+                if (x > st.m[t][i] + Ty::kLag) {  // the same decision in the eight lanes of a row
+                    const float a = ex2_approx(st.m[t][i] - x);  // 0 from -inf
+                    st.m[t][i] = x;
+                    st.l[t][i] *= a;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        st.o[t][e][i] *= a;
+                        st.o[t][e][2 + i] *= a;
+                    }
+                }
+            }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float sub = st.m[t][i] == -INFINITY ? 0.f : st.m[t][i] - Ty::kShift;
+            p[i] = ex2_approx(fmaf(s[t][i], sl2, -sub));
+            p[2 + i] = ex2_approx(fmaf(s[t][2 + i], sl2, -sub));
+            st.l[t][i] += p[i] + p[2 + i];
+        }
+        // P is rounded to the cache's type for the product (half a step, 2^-8 of a
+        // bf16 weight: the size of the output's own rounding); the sum keeps fp32
+        pb[t][0] = transpose8x8(Ty::pack(p[0], p[1]));
+        pb[t][1] = transpose8x8(Ty::pack(p[2], p[3]));
+    }
+    // vr[2 k + half]: key (2c, 2c + 1, 2c + 8, 2c + 9)[k], channels 64 half + 8 r ..
+    const uint32_t *v = reinterpret_cast<const uint32_t *>(vr);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
+        const int w = e >> 1;
+        const uint32_t a0 = __byte_perm(v[0 + w], v[8 + w], sel), a1 = __byte_perm(v[4 + w], v[12 + w], sel);
+        const uint32_t a2 = __byte_perm(v[16 + w], v[24 + w], sel), a3 = __byte_perm(v[20 + w], v[28 + w], sel);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) Ty::mma(st.o[t][e], a0, a1, a2, a3, pb[t][0], pb[t][1]);
+    }
+}
+
+// Groups g0 .. g1 - 1 of an item, joined over the CTA's warps; the result goes to
+// the output, or to partial slot `slot` (>= 0).
+template <class Ty, int NT, bool kSparse>
+__device__ __forceinline__ void run_piece(const PagedAttnParams &P, const Item &it, const int *list, int n_list,
+                                          int g0, int g1, int slot, float *sm_o, float2 *sm_ml) {
+    using T = typename Ty::T;
+    const PagedSeqs &S = P.seqs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int gp_log2 = S.page_log2 - 4;  // 16-key groups per page
+
+    // query fragments: row r of each 8-row tile, channels 8 (c + 4 i)
+    uint4 qf[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int x = it.row0 + t * 8 + r;
+        const bool in = t * 8 + r < it.rows;
+        const T *src = static_cast<const T *>(P.q) + (long long)(it.tok0 + x / P.group) * P.q_ts +
+                       (long long)(it.h * P.group + x % P.group) * P.q_hs + c * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            qf[t][i] = in ? __ldg(reinterpret_cast<const uint4 *>(src + i * 32)) : make_uint4(0, 0, 0, 0);
+    }
+    // keys each of this lane's score columns sees
+    int lim[NT][2], min_lim = it.pos0 + it.row0 / P.group + 1;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int x = min(it.row0 + t * 8 + 2 * c + i, it.row0 + it.rows - 1);
+            lim[t][i] = it.pos0 + x / P.group + 1;
+        }
+    State<Ty, NT> st;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        st.m[t][0] = st.m[t][1] = -INFINITY;
+        st.l[t][0] = st.l[t][1] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st.o[t][e][i] = 0.f;
+    }
+
+    PageWalk<kSparse> walk;
+    walk.S = &S;
+    walk.hdr = P.hdr;
+    walk.list = list;
+    walk.seq = it.seq;
+    walk.last_blk = kSparse ? it.pos0 >> S.page_log2 : 0;
+    walk.n_slots = kSparse ? n_list : (it.len + S.page - 1) >> S.page_log2;
+    walk.start((g0 + warp) >> gp_log2, lane);
+
+    const T *kc = static_cast<const T *>(P.k) + (long long)it.h * S.page * kD + r * kD + c * 8;
+    const T *vc = static_cast<const T *>(P.v) + (long long)it.h * S.page * kD + 2 * c * kD + r * 8;
+    const int gp_mask = (1 << gp_log2) - 1;
+
+    uint4 kr[8], kn[8], vr[8];
+    int blk, pg, nblk = -1, npg = -1;
+    auto load_k = [&](uint4(&dst)[8], int page, int g) {
+        const T *src = kc + (long long)page * P.kc_ps + (g & gp_mask) * (kGroup * kD);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            dst[i] = ldg_stream(src + i * 32);
+            dst[4 + i] = ldg_stream(src + 8 * kD + i * 32);
+        }
+    };
+    auto load_v = [&](int page, int g, int key0) {
+        const T *src = vc + (long long)page * P.vc_ps + (g & gp_mask) * (kGroup * kD);
+        const bool tail = key0 + kGroup > it.len;  // rows past the stored tokens may hold anything
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int key = (k & 1) + (k >> 1) * 8;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                vr[2 * k + hf] = ldg_stream(src + key * kD + hf * 64);
+                if (tail && key0 + 2 * c + key >= it.len) vr[2 * k + hf] = make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+    int g = g0 + warp;
+    if (g < g1) {
+        walk.get(g >> gp_log2, lane, blk, pg);
+        if (pg >= 0) load_k(kr, pg, g);
+        for (; g < g1; g += kWarps) {
+            const int key0 = (blk << S.page_log2) + (g & gp_mask) * kGroup;
+            const bool live = pg >= 0 && key0 < it.len;
+            if (live) load_v(pg, g, key0);
+            if (g + kWarps < g1) {
+                walk.get((g + kWarps) >> gp_log2, lane, nblk, npg);
+                if (npg >= 0) load_k(kn, npg, g + kWarps);
+            }
+            if (live) step<Ty, NT>(st, kr, vr, qf, key0, lim, min_lim, P.scale_log2, lane);
+            blk = nblk;
+            pg = npg;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) kr[i] = kn[i];
+        }
+    }
+
+    // ---- join the warps
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float l = st.l[t][i];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            if (r == 0) sm_ml[warp * 8 * NT + t * 8 + 2 * c + i] = make_float2(st.m[t][i], l);
+            float *dst = sm_o + (size_t)(warp * 8 * NT + t * 8 + 2 * c + i) * kOPad + 8 * r;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int e = 0; e < 8; e += 4)
+                    *reinterpret_cast<float4 *>(dst + hf * 64 + e) =
+                        make_float4(st.o[t][e][2 * hf + i], st.o[t][e + 1][2 * hf + i], st.o[t][e + 2][2 * hf + i],
+                                    st.o[t][e + 3][2 * hf + i]);
+        }
+    __syncthreads();
+    for (int row = warp; row < it.rows; row += kWarps) {
+        float2 ml[kWarps];
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            ml[w] = sm_ml[w * 8 * NT + row];
+            m = fmaxf(m, ml[w].x);
+        }
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float a = ml[w].x == -INFINITY ? 0.f : ex2_approx(ml[w].x - m);
+            const float4 x = *reinterpret_cast<const float4 *>(sm_o + (size_t)(w * 8 * NT + row) * kOPad + lane * 4);
+            l = fmaf(ml[w].y, a, l);
+            o.x = fmaf(x.x, a, o.x);
+            o.y = fmaf(x.y, a, o.y);
+            o.z = fmaf(x.z, a, o.z);
+            o.w = fmaf(x.w, a, o.w);
+        }
+        if (slot >= 0) {
+            reinterpret_cast<float4 *>(P.part_o)[((size_t)slot * 8 * NT + row) * 32 + lane] = o;
+            if (lane == 0) P.part_ml[(size_t)slot * 8 * NT + row] = make_float2(m, l);
+        } else {
+            const int x = it.row0 + row, tok = it.tok0 + x / P.group, hh = it.h * P.group + x % P.group;
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays one
+            uint2 *dst = reinterpret_cast<uint2 *>(static_cast<T *>(P.out) + (long long)tok * P.o_ts +
+                                                   (long long)hh * P.o_hs) + lane;
+            *dst = make_uint2(Ty::pack(o.x * inv, o.y * inv), Ty::pack(o.z * inv, o.w * inv));
+            if (lane == 0 && P.lse)
+                P.lse[(size_t)tok * P.hq + hh] =
+                    l == 0.f ? -INFINITY : (m - Ty::kShift + __log2f(l)) * 0.69314718055994531f;
+        }
+    }
+    __syncthreads();  // the buffers are free for the next piece
+}
+
+template <int NT>
+constexpr int join_bytes() {
+    return kWarps * 8 * NT * (kOPad * 4 + 8);
+}
+
+// ------------------------------------------------------------------ dense
+// Work units: 16-key groups, sequence after sequence; within one, (kv-head, row
+// tile) after one another.  CTA c of C takes units [U c / C, U (c + 1) / C).
+template <class Ty, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_dense_kernel(const __grid_constant__ PagedAttnParams P) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    float *sm_o = reinterpret_cast<float *>(smem);
+    float2 *sm_ml = reinterpret_cast<float2 *>(smem + kWarps * 8 * NT * kOPad * 4);
+    long long *pre = reinterpret_cast<long long *>(smem + join_bytes<NT>());  // [n_seqs + 1] units before sequence s
+    __shared__ long long warp_sum[kWarps];
+    const PagedSeqs &S = P.seqs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const int per = (S.n_seqs + kThreads - 1) / kThreads;
+    const int sa = min(threadIdx.x * per, S.n_seqs), sb = min(sa + per, S.n_seqs);
+    auto units = [&](int s) -> long long {
+        const SeqView v = seq_view(S, s, P.hdr);
+        const int tiles = (v.n * P.group + 8 * NT - 1) / (8 * NT);
+        return (long long)tiles * P.hkv * ((v.len + kGroup - 1) / kGroup);
+    };
+    long long mine = 0;
+    for (int s = sa; s < sb; ++s) mine += units(s);
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    long long at = inc - mine;
+    for (int w = 0; w < warp; ++w) at += warp_sum[w];
+    for (int s = sa; s < sb; ++s) {
+        pre[s] = at;
+        at += units(s);
+    }
+    if (threadIdx.x == 0) {
+        long long t = 0;
+        for (int w = 0; w < kWarps; ++w) t += warp_sum[w];
+        pre[S.n_seqs] = t;
+    }
+    __syncthreads();
+    const long long total = pre[S.n_seqs];
+    const int rt_max = (S.max_q * P.group + 8 * NT - 1) / (8 * NT);
+
+    // sequences with new tokens and nothing stored: their rows see no key
+    for (int s = blockIdx.x; s < S.n_seqs; s += gridDim.x) {
+        const SeqView v = seq_view(S, s, P.hdr);
+        if (v.n == 0 || v.len > 0) continue;
+        for (int i = threadIdx.x; i < v.n * P.hq * 16; i += kThreads) {
+            const int row = i >> 4, tok = v.q0 + row / P.hq, hh = row % P.hq;
+            reinterpret_cast<uint4 *>(static_cast<typename Ty::T *>(P.out) + (long long)tok * P.o_ts +
+                                      (long long)hh * P.o_hs)[i & 15] = make_uint4(0, 0, 0, 0);
+            if ((i & 15) == 0 && P.lse) P.lse[(size_t)tok * P.hq + hh] = -INFINITY;
+        }
+        for (int i = threadIdx.x; i < P.hkv * rt_max; i += kThreads)
+            P.part_item[P.n_slots + s * P.hkv * rt_max + i] = -1;
+    }
+
+    // CTAs that share the units: one 16-key group to a warp at least, so that none of
+    // them is without work (an item's parts then sit in consecutive CTAs)
+    const long long n_cta = min((long long)gridDim.x, max(1ll, total / kWarps));
+    const long long me = min((long long)blockIdx.x, n_cta);
+    const long long u0 = total * me / n_cta, u1 = total * min(me + 1, n_cta) / n_cta;
+    int slot_item[2] = {-1, -1};
+    int n_piece = 0;
+    long long u = u0;
+    int s = 0;
+    {
+        int lo = 0, hi = S.n_seqs;  // last sequence starting at or before u
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= u) lo = mid;
+            else hi = mid;
+        }
+        s = lo;
+    }
+    while (u < u1) {
+        while (pre[s + 1] <= u) ++s;  // also steps over sequences without units
+        const SeqView v = seq_view(S, s, P.hdr);
+        const int groups = (v.len + kGroup - 1) / kGroup;
+        const int tiles = (v.n * P.group + 8 * NT - 1) / (8 * NT);
+        const long long rem = u - pre[s];
+        const int in_seq = (int)(rem / groups), ga = (int)(rem % groups);
+        const int gb = (int)min((long long)groups, ga + (u1 - u));
+        Item it;
+        it.seq = s;
+        it.h = in_seq / tiles;
+        it.row0 = (in_seq % tiles) * 8 * NT;
+        it.rows = min(8 * NT, v.n * P.group - it.row0);
+        it.tok0 = v.q0;
+        it.pos0 = v.len - v.n;
+        it.len = v.len;
+        const int id = (s * P.hkv + it.h) * rt_max + in_seq % tiles;
+        const bool whole = ga == 0 && gb == groups;
+        const int which = n_piece == 0 ? 0 : 1;  // a cut piece is a CTA's first or its last
+        const int slot = whole ? -1 : 2 * (int)blockIdx.x + which;
+        if (!whole) slot_item[which] = id;
+        // the item's first slot, for the joining kernel (-1: already whole)
+        if (ga == 0 && threadIdx.x == 0) P.part_item[P.n_slots + id] = slot;
+        run_piece<Ty, NT, false>(P, it, nullptr, 0, ga, gb, slot, sm_o, sm_ml);
+        u += gb - ga;
+        ++n_piece;
+    }
+    if (threadIdx.x < 2) P.part_item[2 * blockIdx.x + threadIdx.x] = threadIdx.x ? slot_item[1] : slot_item[0];
+}
+
+// ------------------------------------------------------------------ selected pages
+// One CTA per (token, kv-head, row tile) and part of its page list.
+template <class Ty, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_sparse_kernel(const __grid_constant__ PagedAttnParams P) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    float *sm_o = reinterpret_cast<float *>(smem);
+    float2 *sm_ml = reinterpret_cast<float2 *>(smem + kWarps * 8 * NT * kOPad * 4);
+    __shared__ int found;
+    const PagedSeqs &S = P.seqs;
+    const int part = blockIdx.x % P.parts, item = blockIdx.x / P.parts;
+    const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
+    const int rt = item % tiles, h = (item / tiles) % P.hkv, t = item / tiles / P.hkv;
+    if (threadIdx.x == 0) found = -1;
+    __syncthreads();
+    for (int s = threadIdx.x; s < S.n_seqs; s += kThreads)
+        if (__ldg(S.cu_q + s) <= t && t < __ldg(S.cu_q + s + 1)) found = s;
+    __syncthreads();
+    const int s = found;
+    if (s < 0) return;  // a row behind the last sequence
+    const SeqView v = seq_view(S, s, P.hdr);
+    if (v.n == 0) return;
+    Item it;
+    it.seq = s;
+    it.h = h;
+    it.row0 = rt * 8 * NT;
+    it.rows = min(8 * NT, P.group - it.row0);
+    it.tok0 = t;
+    it.pos0 = v.len - v.n + (t - v.q0);
+    it.len = v.len;
+    const int li = t * P.hkv + h;
+    int cnt = __ldg(P.blk_cnt + li);
+    if (cnt < 0 || cnt > P.topk) {
+        flag_invalid(P.hdr, BAD_BLOCK);
+        cnt = max(0, min(cnt, P.topk));
+    }
+    if (it.pos0 < 0) cnt = 0;
+    const int gp = S.page >> 4;
+    const int a = (int)((long long)cnt * part / P.parts), b = (int)((long long)cnt * (part + 1) / P.parts);
+    run_piece<Ty, NT, true>(P, it, P.blk_idx + (long long)li * P.topk, cnt, a * gp, b * gp,
+                            P.parts > 1 ? item * P.parts + part : -1, sm_o, sm_ml);
+}
+
+// ------------------------------------------------------------------ join
+// One CTA per (item, row): the parts in order, a quarter of them to each warp.
+template <class Ty, int NT, bool kSparse>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams P) {
+    __shared__ float4 so[kWarps][32];
+    __shared__ float sl[kWarps];
+    const PagedSeqs &S = P.seqs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int id = blockIdx.x, row = blockIdx.y;
+    int h, x, tok0, first, n_part;
+    if (kSparse) {
+        const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
+        h = (id / tiles) % P.hkv;
+        x = (id % tiles) * 8 * NT + row;
+        tok0 = id / tiles / P.hkv;
+        if (x >= P.group) return;
+        // rows behind the last sequence, and rows of one left out, are not written
+        int hit = -1;
+        for (int s = threadIdx.x; s < S.n_seqs; s += kThreads)
+            if (__ldg(S.cu_q + s) <= tok0 && tok0 < __ldg(S.cu_q + s + 1) && seq_view(S, s, P.hdr).n > 0) hit = s;
+        if (!__syncthreads_or(hit >= 0)) return;
+        first = id * P.parts;
+        n_part = P.parts;
+    } else {
+        const int rt_max = (S.max_q * P.group + 8 * NT - 1) / (8 * NT);
+        const int s = id / rt_max / P.hkv;
+        h = (id / rt_max) % P.hkv;
+        x = (id % rt_max) * 8 * NT + row;
+        const SeqView v = seq_view(S, s, P.hdr);
+        tok0 = v.q0;
+        if (x >= v.n * P.group) return;
+        first = P.part_item[P.n_slots + id];
+        if (first < 0) return;
+        n_part = 1;
+        for (int i0 = 1;; i0 += 32) {  // the parts that follow sit in every second slot
+            const int sl_i = 2 * (first / 2 + i0 + lane);
+            const bool same = sl_i < P.n_slots && P.part_item[sl_i] == id;
+            const unsigned bal = __ballot_sync(0xffffffffu, same);
+            const int run = bal == 0xffffffffu ? 32 : __ffs(~bal) - 1;
+            n_part += run;
+            if (run < 32) break;
+        }
+    }
+    auto slot_of = [&](int i) -> size_t {
+        const int sidx = kSparse ? first + i : (i == 0 ? first : 2 * (first / 2 + i));
+        return (size_t)sidx * 8 * NT + row;
+    };
+    float m = -INFINITY;
+    for (int i = lane; i < n_part; i += 32) m = fmaxf(m, P.part_ml[slot_of(i)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = warp; i < n_part; i += kWarps) {
+        const size_t si = slot_of(i);
+        const float2 ml = P.part_ml[si];
+        const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+        const float4 o = reinterpret_cast<const float4 *>(P.part_o)[si * 32 + lane];
+        l = fmaf(ml.y, a, l);
+        acc.x = fmaf(o.x, a, acc.x);
+        acc.y = fmaf(o.y, a, acc.y);
+        acc.z = fmaf(o.z, a, acc.z);
+        acc.w = fmaf(o.w, a, acc.w);
+    }
+    so[warp][lane] = acc;
+    if (lane == 0) sl[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+        const float4 o = so[w][lane];
+        acc.x += o.x;
+        acc.y += o.y;
+        acc.z += o.z;
+        acc.w += o.w;
+        l += sl[w];
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const int tok = tok0 + x / P.group, hh = h * P.group + x % P.group;
+    uint2 *dst = reinterpret_cast<uint2 *>(static_cast<typename Ty::T *>(P.out) + (long long)tok * P.o_ts +
+                                           (long long)hh * P.o_hs) + lane;
+    *dst = make_uint2(Ty::pack(acc.x * inv, acc.y * inv), Ty::pack(acc.z * inv, acc.w * inv));
+    if (lane == 0 && P.lse)
+        P.lse[(size_t)tok * P.hq + hh] = l == 0.f ? -INFINITY : (m - Ty::kShift + __log2f(l)) * 0.69314718055994531f;
+}
+
+template <class Ty, int NT>
+cudaError_t launch_dense(const PagedAttnParams &P, cudaStream_t st) {
+    const PagedSeqs &S = P.seqs;
+    const int bytes = join_bytes<NT>() + (S.n_seqs + 1) * (int)sizeof(long long);
+    cudaError_t e = cudaFuncSetAttribute(paged_dense_kernel<Ty, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         join_bytes<NT>() + (kMaxSeqs + 1) * (int)sizeof(long long));
+    if (e != cudaSuccess) return e;
+    const int rt = (S.max_q * P.group + 8 * NT - 1) / (8 * NT);
+    ProfScope prof("paged_dense", st);
+    paged_dense_kernel<Ty, NT><<<kStreamGrid, kThreads, bytes, st>>>(P);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const dim3 grid(S.n_seqs * P.hkv * rt, min(8 * NT, S.max_q * P.group));
+    paged_join_kernel<Ty, NT, false><<<grid, kThreads, 0, st>>>(P);
+    return cudaGetLastError();
+}
+
+template <class Ty, int NT>
+cudaError_t launch_sparse(const PagedAttnParams &P, cudaStream_t st) {
+    const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
+    const long long items = (long long)P.seqs.total * P.hkv * tiles;
+    if (items * P.parts > 0x7fffffffll) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(paged_sparse_kernel<Ty, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         join_bytes<NT>());
+    if (e != cudaSuccess) return e;
+    ProfScope prof("paged_sparse", st);
+    paged_sparse_kernel<Ty, NT><<<(unsigned)(items * P.parts), kThreads, join_bytes<NT>(), st>>>(P);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || P.parts == 1) return e;
+    paged_join_kernel<Ty, NT, true><<<dim3((unsigned)items, min(8 * NT, P.group)), kThreads, 0, st>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+StreamPlan paged_stream_plan(int n_seqs, int hkv, int group, int max_q) {
+    StreamPlan p{};
+    p.rows = max_q * group <= 8 ? 8 : 16;
+    p.parts = 1;
+    p.n_slots = 2 * kStreamGrid;
+    p.n_items = (long long)n_seqs * hkv * ((max_q * group + p.rows - 1) / p.rows);
+    return p;
+}
+
+StreamPlan paged_sparse_plan(int total, int hkv, int group, int topk, int page) {
+    StreamPlan p{};
+    p.rows = group <= 8 ? 8 : 16;
+    const long long items = (long long)total * hkv * ((group + p.rows - 1) / p.rows);
+    // parts until the machine is filled, at least one 16-key group to a warp
+    long long parts = items > 0 ? (kStreamGrid + items - 1) / items : 1;
+    parts = min(parts, max(1ll, (long long)topk * page / (kGroup * kWarps)));
+    p.parts = (int)min(parts, (long long)topk);
+    p.n_slots = p.parts > 1 ? (int)(items * p.parts) : 0;
+    p.n_items = 0;
+    return p;
+}
+
+cudaError_t run_paged_stream(const PagedAttnParams &P, bool fp16, int rows, cudaStream_t st) {
+    if (P.seqs.n_seqs == 0 || P.seqs.total == 0) return cudaSuccess;
+    if (fp16) return rows == 8 ? launch_dense<Fp16, 1>(P, st) : launch_dense<Fp16, 2>(P, st);
+    return rows == 8 ? launch_dense<Bf16, 1>(P, st) : launch_dense<Bf16, 2>(P, st);
+}
+
+cudaError_t run_paged_sparse(const PagedAttnParams &P, bool fp16, int rows, cudaStream_t st) {
+    if (P.seqs.n_seqs == 0 || P.seqs.total == 0) return cudaSuccess;
+    if (fp16) return rows == 8 ? launch_sparse<Fp16, 1>(P, st) : launch_sparse<Fp16, 2>(P, st);
+    return rows == 8 ? launch_sparse<Bf16, 1>(P, st) : launch_sparse<Bf16, 2>(P, st);
+}
+
+}  // namespace minf

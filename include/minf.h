@@ -74,6 +74,10 @@ typedef struct CUstream_st *minf_stream_t; /* the same type as cudaStream_t */
 #define MINF_OP_DENSE_ATTENTION 6
 #define MINF_OP_MIXED_LAYER 7
 #define MINF_OP_TRISHAPE_ATTENTION 8
+#define MINF_OP_PAGED_APPEND 9
+#define MINF_OP_PAGED_ATTENTION 10
+#define MINF_OP_PAGED_BLOCK_ESTIMATE 11
+#define MINF_OP_PAGED_BLOCK_ATTENTION 12
 
 /* Per-head pattern codes for minf_mixed_layer. */
 #define MINF_PATTERN_DENSE 0
@@ -257,10 +261,140 @@ int minf_mixed_layer(const minf_bf16 *q, const minf_bf16 *k, const minf_bf16 *v,
                      minf_bf16 *out, float *lse, void *ws, size_t ws_bytes,
                      minf_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key/value cache: the steps after the prompt.
+ *
+ * The cache holds pages of P = page_size tokens, [num_pages][hkv][P][128] for
+ * keys and for values; a sequence's token at position p is row p % P of page
+ * block_tables[s][p / P].  The new tokens of sequence s are rows
+ * cu_q[s] .. cu_q[s + 1] - 1 of the row tensors, at positions
+ * kv_lens[s] - n .. kv_lens[s] - 1 (n = cu_q[s + 1] - cu_q[s]): kv_lens counts
+ * them as stored.  None of this has a counterpart in the method's sources,
+ * which stop at the prompt ([TALK] only names the stages that follow it).
+ *
+ * Common to the four calls:
+ *   - dtype is MINF_BF16 or MINF_FP16, for rows and cache alike; d must be 128;
+ *     at most 128 q-heads to a kv-head.
+ *   - Row tensors are [tokens][heads][128] with any positive strides that are
+ *     multiples of 8 elements (both [tokens][heads] and [heads][tokens]
+ *     layouts, and slices of a fused projection); written ones must not overlap
+ *     themselves.  All base addresses are 16-byte aligned.
+ *   - cu_q, kv_lens, block_tables (and page lists) are DEVICE arrays, read when
+ *     the kernels run: a captured graph may be replayed with other contents.
+ *     What they say is checked there.  A sequence with n < 0, n > max_q, rows
+ *     outside [0, total) or kv_lens outside [0, width * page_size] is left out;
+ *     a page number outside [0, num_pages) is left out by the append, and the
+ *     keys concerned are unspecified in the others; MINF_ERR_INVALID is then
+ *     recorded in the workspace's status word (minf_status).
+ *   - Sequences may have no new tokens.  Rows that belong to no sequence (behind
+ *     cu_q[n_seqs]) are neither read nor written.
+ *   - kv_lens[s] < n is allowed in all but the append: tokens whose position is
+ *     negative see no key (out 0, lse -inf, an empty page list).
+ *   - Page slots at and behind a sequence's kv_lens may hold anything, NaN
+ *     included.  Keys and values of stored positions must be finite.
+ *   - The workspace is as everywhere: at least minf_paged_workspace_bytes, its
+ *     first MINF_STATUS_BYTES zero before its first use, used by one call at a
+ *     time (also by one captured graph's replay at a time).
+ *   - The caller's current device is left as it was.
+ */
+#define MINF_BF16 0
+#define MINF_FP16 1
+
+typedef struct {
+    const int32_t *cu_q;         /* [n_seqs + 1] */
+    const int32_t *kv_lens;      /* [n_seqs] */
+    const int32_t *block_tables; /* [n_seqs][width], rows table_stride apart */
+    int64_t table_stride;        /* in elements, at least width */
+    int32_t width;               /* pages a table row can name; width * page_size <= 2^30 */
+    int32_t n_seqs;              /* at most 4096 */
+    int32_t total;               /* rows of the row tensors */
+    int32_t max_q;               /* bound on the new tokens of a sequence, 1 .. total */
+    int32_t page_size;           /* 16, 32, 64 or 128 */
+    int32_t num_pages;
+} minf_paged_seqs;
+
+typedef struct {
+    void *data; /* [tokens][heads][128] */
+    int64_t token_stride, head_stride;
+} minf_rows;
+
+typedef struct {
+    void *k, *v;                           /* [num_pages][hkv][page_size][128] */
+    int64_t k_page_stride, v_page_stride;  /* in elements, at least hkv * page_size * 128 */
+} minf_paged_cache;
+
+/*
+ * Bytes of workspace of a paged call (MINF_OP_PAGED_*; topk for the two block
+ * operations, width for the estimate).  0 for arguments the call would reject.
+ */
+size_t minf_paged_workspace_bytes(int op, int hq, int hkv, int total, int n_seqs, int max_q, int width,
+                                  int topk);
+
+/*
+ * Stores the new tokens' keys and values.  With `rope` (fp32, device,
+ * [rope_rows][rot]: the cosines of a position in the first half of its row, the
+ * sines in the second), the first `rot` channels of every key are rotated
+ * first, in fp32: y_a = x_a cos - x_b sin, y_b = x_b cos + x_a sin for the pairs
+ * (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) with `interleaved`; rot is a
+ * multiple of 16, at most 128, and a sequence whose kv_lens exceeds rope_rows is
+ * left out (MINF_ERR_INVALID).  With `rope` NULL nothing is rotated.  With `q`
+ * (and `q_out`, which may be `q` itself) the queries are rotated too.  With
+ * `k_bounds` (same type, [num_pages][hkv][2][128]) each page touched keeps its
+ * channels' smallest and largest stored key: over the new keys where the first
+ * of them is the page's row 0, else joined with what k_bounds held.  Sequences
+ * must not append to a page that another one appends to in the same call.
+ */
+int minf_paged_append(const minf_paged_seqs *seqs, int dtype, int hq, int hkv, int d, const minf_rows *k,
+                      const minf_rows *v, const minf_rows *q, const minf_rows *q_out,
+                      const minf_paged_cache *cache, void *k_bounds, const float *rope, int rope_rows,
+                      int rot, int interleaved, void *ws, size_t ws_bytes, minf_stream_t stream);
+
+/*
+ * Causal attention of the new tokens over everything stored, themselves
+ * included: the token at position p attends to positions 0 .. p.  q-head h
+ * reads kv-head h / (hq / hkv).  out like q; lse fp32 [total][hq], nullable
+ * (natural log of the softmax denominator, -inf for a row with no key).  Calls
+ * of few rows per kv-head (max_q * hq / hkv <= 16: decoding) and of more run
+ * different kernels; both split long sequences over the GPU and join the parts
+ * in a fixed order, so equal calls give equal bits.
+ */
+int minf_paged_attention(const minf_paged_seqs *seqs, int dtype, int hq, int hkv, int d, const minf_rows *q,
+                         const minf_paged_cache *cache, float scale, const minf_rows *out, float *lse,
+                         void *ws, size_t ws_bytes, minf_stream_t stream);
+
+/*
+ * Page selection for every new token from the bounds minf_paged_append keeps.
+ * For the token at position p and kv-head h, page j < p / P scores
+ *     sum over the group's q-heads g and channels c of
+ *         max(q[g][c] * min[j][c], q[g][c] * max[j][c]),
+ * an upper bound of the group's summed q . k of any key in the page.  The
+ * token's own page p / P is always kept; the best topk - 1 earlier pages join it,
+ * by exact score (ties to the lower page).  Output, ASCENDING, -1 padded:
+ *   blk_idx int32 [total][hkv][topk], blk_cnt int32 [total][hkv].
+ * width at most 32768.
+ */
+int minf_paged_block_estimate(const minf_paged_seqs *seqs, int dtype, int hq, int hkv, int d,
+                              const minf_rows *q, const void *k_bounds, int topk, int32_t *blk_idx,
+                              int32_t *blk_cnt, void *ws, size_t ws_bytes, minf_stream_t stream);
+
+/*
+ * Causal attention of every new token over the listed pages only: the token at
+ * position p attends, for kv-head h, to the positions k <= p whose page k / P is
+ * among blk_idx[t][h][0 .. blk_cnt[t][h]).  Lists must be ascending with distinct
+ * entries (as minf_paged_block_estimate writes them); an entry that is negative,
+ * past the token's own page or not above the one before it is left out.
+ */
+int minf_paged_block_attention(const minf_paged_seqs *seqs, int dtype, int hq, int hkv, int d,
+                               const minf_rows *q, const minf_paged_cache *cache, float scale,
+                               const int32_t *blk_idx, const int32_t *blk_cnt, int topk,
+                               const minf_rows *out, float *lse, void *ws, size_t ws_bytes,
+                               minf_stream_t stream);
+
 /*
  * Synchronises `stream`, then returns the device-side status word of the
- * workspace: MINF_OK, or MINF_ERR_TIMEOUT if a bounded wait in a kernel gave up
- * (that kernel then left its outputs incomplete).  Reading it resets it to
+ * workspace: MINF_OK, MINF_ERR_TIMEOUT if a bounded wait in a kernel gave up
+ * (that kernel then left its outputs incomplete), or MINF_ERR_INVALID if a paged
+ * call found bad lengths, pages or lists on the device.  Reading it resets it to
  * MINF_OK.  Returns MINF_ERR_CUDA if the synchronisation itself failed.
  */
 int minf_status(void *ws, minf_stream_t stream);
