@@ -129,7 +129,22 @@ struct Fp16 {
     static constexpr float kShift = 10.f, kLag = 4.f;
 };
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint32_t bar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
 // ------------------------------------------------------------------ launches
+// TMA descriptors with 128-byte swizzle: any 4-D 16-bit tensor (strides in bytes),
+// and the pages of a cache, {128, P, hkv, pages} with `rows` keys x 64 channels a box.
+cudaError_t make_tmap_4d(CUtensorMap *map, const void *base, bool fp16, const cuuint64_t (&dims)[4],
+                         const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]);
+cudaError_t make_tmap_pages(CUtensorMap *map, const void *base, bool fp16, int page, int hkv, int num_pages,
+                            long long page_stride, int rows);
+
 struct AppendParams {
     PagedSeqs seqs;
     const void *k, *v, *q;

@@ -190,6 +190,24 @@ int fill_attn(PagedAttnParams &P, const minf_paged_seqs *seqs, int dtype, int hq
 
 }  // namespace
 
+cudaError_t make_tmap_4d(CUtensorMap *map, const void *base, bool fp16, const cuuint64_t (&dims)[4],
+                         const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
+    if (!tmap_encoder()) return cudaErrorNotSupported;
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    const CUresult r = tmap_encoder()(
+        map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
+        dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_pages(CUtensorMap *map, const void *base, bool fp16, int page, int hkv, int num_pages,
+                            long long page_stride, int rows) {
+    return make_tmap_4d(map, base, fp16, {kD, (cuuint64_t)page, (cuuint64_t)hkv, (cuuint64_t)num_pages},
+                        {kD * 2, (cuuint64_t)page * kD * 2, (cuuint64_t)page_stride * 2},
+                        {64, (cuuint32_t)rows, 1, 1});
+}
+
 }  // namespace minf
 
 using namespace minf;

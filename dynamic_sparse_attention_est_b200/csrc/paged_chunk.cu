@@ -57,14 +57,6 @@ constexpr uint32_t idesc(uint32_t type, bool b_mn_major) {
     return (1u << 4) | type | ((b_mn_major ? 1u : 0u) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint32_t bar, int x, int y, int z, int w) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
-        : "memory");
-}
-
 struct ChunkParams {
     CUtensorMap tmap_q;  // {128, G, total, hkv}, box {64, G, tokens per tile, 1}
     CUtensorMap tmap_k;  // {128, P, hkv, pages}, box {64, min(P, 64), 1, 1}
@@ -603,17 +595,6 @@ __global__ void __launch_bounds__(256) paged_chunk_join_kernel(const __grid_cons
     }
 }
 
-cudaError_t encode_4d(CUtensorMap *map, const void *base, bool fp16, const cuuint64_t (&dims)[4],
-                      const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
-    if (!tmap_encoder()) return cudaErrorNotSupported;
-    const cuuint32_t one[4] = {1, 1, 1, 1};
-    const CUresult r = tmap_encoder()(
-        map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
-        dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <class Ty>
 cudaError_t launch_chunk(const ChunkParams &C, cudaStream_t st) {
     const PagedSeqs &S = C.a.seqs;
@@ -657,15 +638,12 @@ cudaError_t run_paged_chunk(const PagedAttnParams &P, bool fp16, int part_rows, 
     const cuuint64_t G = P.group;
     // the stride of a dimension of one element is never used
     const cuuint64_t hs = P.hq > 1 ? P.q_hs : kD, ts = S.total > 1 ? P.q_ts : kD;
-    cudaError_t e = encode_4d(&C.tmap_q, P.q, fp16, {kD, G, (cuuint64_t)S.total, (cuuint64_t)P.hkv},
+    cudaError_t e = make_tmap_4d(&C.tmap_q, P.q, fp16, {kD, G, (cuuint64_t)S.total, (cuuint64_t)P.hkv},
                               {hs * 2, ts * 2, G * hs * 2},
                               {64, (cuuint32_t)P.group, (cuuint32_t)C.tpt, 1});
-    const cuuint64_t dims[4] = {kD, (cuuint64_t)S.page, (cuuint64_t)P.hkv, (cuuint64_t)S.num_pages};
-    const cuuint32_t box[4] = {64, (cuuint32_t)(S.page < 64 ? S.page : 64), 1, 1};
-    if (e == cudaSuccess)
-        e = encode_4d(&C.tmap_k, P.k, fp16, dims, {kD * 2, (cuuint64_t)S.page * kD * 2, (cuuint64_t)P.kc_ps * 2}, box);
-    if (e == cudaSuccess)
-        e = encode_4d(&C.tmap_v, P.v, fp16, dims, {kD * 2, (cuuint64_t)S.page * kD * 2, (cuuint64_t)P.vc_ps * 2}, box);
+    const int box = S.page < 64 ? S.page : 64;
+    if (e == cudaSuccess) e = make_tmap_pages(&C.tmap_k, P.k, fp16, S.page, P.hkv, S.num_pages, P.kc_ps, box);
+    if (e == cudaSuccess) e = make_tmap_pages(&C.tmap_v, P.v, fp16, S.page, P.hkv, S.num_pages, P.vc_ps, box);
     if (e != cudaSuccess) return e;
     return fp16 ? launch_chunk<Fp16>(C, st) : launch_chunk<Bf16>(C, st);
 }

@@ -8,22 +8,22 @@
 // share their pages.  The kernel is built around the loads.
 //
 //   * Warps take 16-key groups and keep a softmax state of their own; nothing
-//     synchronises until the end of an item.  K goes from global memory to the
-//     registers of the matrix instruction without shared memory in between: the
-//     product S^T = K Q^T contracts over channels, in any order that K and Q
-//     share, so a lane's 16 contiguous bytes serve as its fragments.  V^T P^T
-//     contracts over keys; a lane loads 16 bytes of four keys' rows and pairs
-//     them with byte permutes.  The loads of the next group's K and of this
-//     group's V are in flight while this group is computed.
+//     synchronises until the end of an item.  Each warp feeds itself: a ring of
+//     kStages groups (8 KB of K and V each) that its first lane fills by TMA, 192 KB
+//     in flight on an SM.  The boxes are 128-byte swizzled, so ldmatrix reads them
+//     without bank conflicts.
 //   * With keys on the 16-row side and query rows on the 8-column side
-//     (m16n8k16), four or eight q-heads of a group fill the tile, where a
-//     128-row tensor-memory tile would compute 16 to 32 rows for each one used.
+//     (m16n8k16: S^T = K Q^T, then O^T += V^T P^T), four or eight q-heads of a
+//     group fill the tile, where a 128-row tensor-memory tile would compute 16 to
+//     32 rows for each one used.
 //   * Running maximum and sum per row in fp32, log2 domain; the maximum moves
 //     only past a margin, which one vote per group decides.
 //   * Dense items are cut at equal shares of all 16-key groups of the call (each
 //     CTA takes the prefix sums of the lengths itself, so that a captured launch
 //     follows them), however uneven the lengths; an item's parts are joined by a
 //     second small kernel in a fixed order.
+#include <cstring>
+
 #include "internal.h"
 #include "paged.cuh"
 
@@ -34,16 +34,20 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroup = 16;         // keys per warp step
-constexpr int kStreamGrid = 592;   // 148 SMs x 4
+constexpr int kStages = 3;         // groups in flight per warp
+constexpr int kStreamGrid = 296;   // two CTAs (their rings: 192 KB) on each of 148 SMs
 constexpr int kOPad = 132;         // floats per row of the CTA's join buffer
+constexpr uint32_t kBoxBytes = 2048;             // 16 keys x 64 channels
+constexpr uint32_t kStageBytes = 4 * kBoxBytes;  // K low, K high, V low, V high channels
+constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
+constexpr uint32_t kSmemBar = kRingBytes;         // mbarriers, abort flag
+constexpr uint32_t kSmemPre = kSmemBar + 256;     // [n_seqs + 1] units before a sequence (dense)
 
-__device__ __forceinline__ uint4 ldg_stream(const void *p) {
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
-}
+struct StreamParams {
+    CUtensorMap tmap_k;  // {128, P, hkv, pages}, box {64, 16, 1, 1}
+    CUtensorMap tmap_v;
+    PagedAttnParams a;
+};
 
 // 8x8 transpose of 16-bit elements over a warp.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -51,6 +55,22 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// One launch after another may start while the first still runs (its wait below);
+// the first allows it with launch_dependents.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The pages a warp walks: 32 (logical block, page) entries at a time, one per
 // lane, the next 32 already loaded.
@@ -108,45 +128,55 @@ struct State {
     float o[NT][8][4];
 };
 
-// One 16-key group: scores, softmax, P V.
+// One 16-key group at shared address `stage`: scores, softmax, P V.
 template <class Ty, int NT>
-__device__ __forceinline__ void step(State<Ty, NT> &st, const uint4 (&kr)[8], const uint4 (&vr)[8],
-                                     const uint4 (&qf)[NT][4], int key0, const int (&lim)[NT][2], int min_lim,
-                                     float sl2, int lane) {
-    const int r = lane >> 2;
-    float s[NT][4];
+__device__ __forceinline__ void step(State<Ty, NT> &st, uint32_t stage, const uint32_t (&qf)[NT][8][2], int key0,
+                                     const int (&lim)[NT][2], int min_lim, int len, float sl2, int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    float s[2][NT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) s[x][t][i] = 0.f;
+    // K: rows (keys) lane % 16, 16-byte chunk 2 kk + lane / 16 of the 16 in a row
+    {
+        const int row = lane & 15;
+        const uint32_t base = stage + row * 128;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            // kr[i]: key r, channels 8 (c + 4 i) ..; kr[4 + i]: key r + 8
-            Ty::mma(s[t], kr[i].x, kr[4 + i].x, kr[i].y, kr[4 + i].y, qf[t][i].x, qf[t][i].y);
-            Ty::mma(s[t], kr[i].z, kr[4 + i].z, kr[i].w, kr[4 + i].w, qf[t][i].z, qf[t][i].w);
+        for (int kk = 0; kk < 8; ++kk) {
+            uint32_t a[4];
+            const int chunk = (2 * kk & 7) + (lane >> 4);
+            ldmatrix4(a, base + (kk >> 2) * kBoxBytes + ((chunk ^ (row & 7)) << 4));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) Ty::mma(s[kk & 1][t], a[0], a[1], a[2], a[3], qf[t][kk][0], qf[t][kk][1]);
         }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[0][t][i] += s[1][t][i];
+    }
     if (key0 + kGroup > min_lim) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (key0 + r >= lim[t][i]) s[t][i] = -INFINITY;
-                if (key0 + r + 8 >= lim[t][i]) s[t][2 + i] = -INFINITY;
+                if (key0 + r >= lim[t][i]) s[0][t][i] = -INFINITY;
+                if (key0 + r + 8 >= lim[t][i]) s[0][t][2 + i] = -INFINITY;
             }
     }
     bool grow = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) grow |= fmaxf(s[t][i], s[t][2 + i]) * sl2 > st.m[t][i] + Ty::kLag;
+        for (int i = 0; i < 2; ++i) grow |= fmaxf(s[0][t][i], s[0][t][2 + i]) * sl2 > st.m[t][i] + Ty::kLag;
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float x = fmaxf(s[t][i], s[t][2 + i]);
+                float x = fmaxf(s[0][t][i], s[0][t][2 + i]);
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * sl2;
@@ -169,8 +199,8 @@ __device__ __forceinline__ void step(State<Ty, NT> &st, const uint4 (&kr)[8], co
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float sub = st.m[t][i] == -INFINITY ? 0.f : st.m[t][i] - Ty::kShift;
-            p[i] = ex2_approx(fmaf(s[t][i], sl2, -sub));
-            p[2 + i] = ex2_approx(fmaf(s[t][2 + i], sl2, -sub));
+            p[i] = ex2_approx(fmaf(s[0][t][i], sl2, -sub));
+            p[2 + i] = ex2_approx(fmaf(s[0][t][2 + i], sl2, -sub));
             st.l[t][i] += p[i] + p[2 + i];
         }
         // P is rounded to the cache's type for the product (half a step, 2^-8 of a
@@ -178,43 +208,104 @@ __device__ __forceinline__ void step(State<Ty, NT> &st, const uint4 (&kr)[8], co
         pb[t][0] = transpose8x8(Ty::pack(p[0], p[1]));
         pb[t][1] = transpose8x8(Ty::pack(p[2], p[3]));
     }
-    // vr[2 k + half]: key (2c, 2c + 1, 2c + 8, 2c + 9)[k], channels 64 half + 8 r ..
-    const uint32_t *v = reinterpret_cast<const uint32_t *>(vr);
+    // V^T: 16 channels of the 16 keys, transposed on the way
+    const int key = (lane & 7) + ((lane >> 4) << 3), hc = (lane >> 3) & 1;
+    const uint32_t vb = stage + 2 * kBoxBytes + key * 128;
+    const bool tail = key0 + kGroup > len;
+    uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+    if (tail) {  // slots behind the stored tokens may hold anything
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
-        const int w = e >> 1;
-        const uint32_t a0 = __byte_perm(v[0 + w], v[8 + w], sel), a1 = __byte_perm(v[4 + w], v[12 + w], sel);
-        const uint32_t a2 = __byte_perm(v[16 + w], v[24 + w], sel), a3 = __byte_perm(v[20 + w], v[28 + w], sel);
+        for (int x = 0; x < 2; ++x) {
+            const int k = key0 + 8 * x + 2 * c;
+            keep[x] = (k < len ? 0xffffu : 0u) | (k + 1 < len ? 0xffff0000u : 0u);
+        }
+    }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) Ty::mma(st.o[t][e], a0, a1, a2, a3, pb[t][0], pb[t][1]);
+    for (int m = 0; m < 8; ++m) {
+        uint32_t a[4];
+        const int chunk = (2 * m & 7) + hc;
+        ldmatrix4_trans(a, vb + (m >> 2) * kBoxBytes + ((chunk ^ (key & 7)) << 4));
+        if (tail) {
+            a[0] &= keep[0];
+            a[1] &= keep[0];
+            a[2] &= keep[1];
+            a[3] &= keep[1];
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) Ty::mma(st.o[t][m], a[0], a[1], a[2], a[3], pb[t][0], pb[t][1]);
     }
 }
+
+struct Ring {
+    uint32_t stage0, bar0;  // this warp's stages and mbarriers
+    uint32_t phase;         // bit per stage: parity of its next fill
+};
 
 // Groups g0 .. g1 - 1 of an item, joined over the CTA's warps; the result goes to
 // the output, or to partial slot `slot` (>= 0).
 template <class Ty, int NT, bool kSparse>
-__device__ __forceinline__ void run_piece(const PagedAttnParams &P, const Item &it, const int *list, int n_list,
-                                          int g0, int g1, int slot, float *sm_o, float2 *sm_ml) {
+__device__ __forceinline__ void run_piece(const StreamParams &SP, const Item &it, const int *list, int n_list, int g0,
+                                          int g1, int slot, Ring &ring, const WaitCtl &wc, float *sm_o,
+                                          float2 *sm_ml) {
     using T = typename Ty::T;
+    const PagedAttnParams &P = SP.a;
     const PagedSeqs &S = P.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int gp_log2 = S.page_log2 - 4;  // 16-key groups per page
+    const int gp_mask = (1 << gp_log2) - 1;
 
-    // query fragments: row r of each 8-row tile, channels 8 (c + 4 i)
-    uint4 qf[NT][4];
+    PageWalk<kSparse> walk;
+    walk.S = &S;
+    walk.hdr = P.hdr;
+    walk.list = list;
+    walk.seq = it.seq;
+    walk.last_blk = kSparse ? it.pos0 >> S.page_log2 : 0;
+    walk.n_slots = kSparse ? n_list : (it.len + S.page - 1) >> S.page_log2;
+    walk.start((g0 + warp) >> gp_log2, lane);
+
+    int stage_key = -1;  // lane s: first key of the group in stage s, -1 if none
+    auto fill = [&](int st, int g) {
+        int key0 = -1, pg = -1;
+        if (g < g1) {
+            int blk;
+            walk.get(g >> gp_log2, lane, blk, pg);
+            key0 = pg >= 0 ? (blk << S.page_log2) + (g & gp_mask) * kGroup : -1;
+            if (key0 >= it.len) key0 = -1;
+        }
+        if (lane == st) stage_key = key0;
+        if (key0 >= 0 && lane == 0) {
+            const uint32_t bar = ring.bar0 + st * 8, dst = ring.stage0 + st * kStageBytes;
+            const int row = (g & gp_mask) * kGroup;
+            mbar_arrive_expect_tx(bar, kStageBytes);
+            tma_load_4d(dst, &SP.tmap_k, bar, 0, row, it.h, pg);
+            tma_load_4d(dst + kBoxBytes, &SP.tmap_k, bar, 64, row, it.h, pg);
+            tma_load_4d(dst + 2 * kBoxBytes, &SP.tmap_v, bar, 0, row, it.h, pg);
+            tma_load_4d(dst + 3 * kBoxBytes, &SP.tmap_v, bar, 64, row, it.h, pg);
+        }
+    };
+    bool ok = !*wc.abort_flag;
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok)
+#pragma unroll
+        for (int st = 0; st < kStages; ++st) fill(st, g0 + warp + st * kWarps);
+
+    // query fragments: row r of each 8-row tile, channels 16 kk + 2 c, + 1, + 8, + 9
+    uint32_t qf[NT][8][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int x = it.row0 + t * 8 + r;
         const bool in = t * 8 + r < it.rows;
         const T *src = static_cast<const T *>(P.q) + (long long)(it.tok0 + x / P.group) * P.q_ts +
-                       (long long)(it.h * P.group + x % P.group) * P.q_hs + c * 8;
+                       (long long)(it.h * P.group + x % P.group) * P.q_hs + c * 2;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            qf[t][i] = in ? __ldg(reinterpret_cast<const uint4 *>(src + i * 32)) : make_uint4(0, 0, 0, 0);
+        for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                qf[t][kk][i] = in ? __ldg(reinterpret_cast<const unsigned *>(src + kk * 16 + i * 8)) : 0u;
     }
     // keys each of this lane's score columns sees
-    int lim[NT][2], min_lim = it.pos0 + it.row0 / P.group + 1;
+    int lim[NT][2];
+    const int min_lim = it.pos0 + it.row0 / P.group + 1;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -233,63 +324,34 @@ __device__ __forceinline__ void run_piece(const PagedAttnParams &P, const Item &
             for (int i = 0; i < 4; ++i) st.o[t][e][i] = 0.f;
     }
 
-    PageWalk<kSparse> walk;
-    walk.S = &S;
-    walk.hdr = P.hdr;
-    walk.list = list;
-    walk.seq = it.seq;
-    walk.last_blk = kSparse ? it.pos0 >> S.page_log2 : 0;
-    walk.n_slots = kSparse ? n_list : (it.len + S.page - 1) >> S.page_log2;
-    walk.start((g0 + warp) >> gp_log2, lane);
-
-    const T *kc = static_cast<const T *>(P.k) + (long long)it.h * S.page * kD + r * kD + c * 8;
-    const T *vc = static_cast<const T *>(P.v) + (long long)it.h * S.page * kD + 2 * c * kD + r * 8;
-    const int gp_mask = (1 << gp_log2) - 1;
-
-    uint4 kr[8], kn[8], vr[8];
-    int blk, pg, nblk = -1, npg = -1;
-    auto load_k = [&](uint4(&dst)[8], int page, int g) {
-        const T *src = kc + (long long)page * P.kc_ps + (g & gp_mask) * (kGroup * kD);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            dst[i] = ldg_stream(src + i * 32);
-            dst[4 + i] = ldg_stream(src + 8 * kD + i * 32);
-        }
-    };
-    auto load_v = [&](int page, int g, int key0) {
-        const T *src = vc + (long long)page * P.vc_ps + (g & gp_mask) * (kGroup * kD);
-        const bool tail = key0 + kGroup > it.len;  // rows past the stored tokens may hold anything
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int key = (k & 1) + (k >> 1) * 8;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                vr[2 * k + hf] = ldg_stream(src + key * kD + hf * 64);
-                if (tail && key0 + 2 * c + key >= it.len) vr[2 * k + hf] = make_uint4(0, 0, 0, 0);
+    if (ok) {
+        int s = 0;
+        for (int g = g0 + warp; g < g1; g += kWarps) {
+            const int key0 = __shfl_sync(0xffffffffu, stage_key, s);
+            if (key0 >= 0) {
+                const bool got = wait_bounded(ring.bar0 + s * 8, (ring.phase >> s) & 1, wc, wait_site(7, s, g));
+                if (__any_sync(0xffffffffu, !got)) {
+                    ok = false;
+                    break;
+                }
+                ring.phase ^= 1u << s;
+                step<Ty, NT>(st, ring.stage0 + s * kStageBytes, qf, key0, lim, min_lim, it.len, P.scale_log2, lane);
+                __syncwarp();  // every lane has read the stage
             }
+            fill(s, g + kStages * kWarps);
+            s = s == kStages - 1 ? 0 : s + 1;
         }
-    };
-    int g = g0 + warp;
-    if (g < g1) {
-        walk.get(g >> gp_log2, lane, blk, pg);
-        if (pg >= 0) load_k(kr, pg, g);
-        for (; g < g1; g += kWarps) {
-            const int key0 = (blk << S.page_log2) + (g & gp_mask) * kGroup;
-            const bool live = pg >= 0 && key0 < it.len;
-            if (live) load_v(pg, g, key0);
-            if (g + kWarps < g1) {
-                walk.get((g + kWarps) >> gp_log2, lane, nblk, npg);
-                if (npg >= 0) load_k(kn, npg, g + kWarps);
-            }
-            if (live) step<Ty, NT>(st, kr, vr, qf, key0, lim, min_lim, P.scale_log2, lane);
-            blk = nblk;
-            pg = npg;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) kr[i] = kn[i];
+        if (!ok) {  // let the loads in flight land before the CTA exits
+            volatile int no_abort = 0;
+            const WaitCtl drain{&no_abort, nullptr, 50000000ull};
+            for (int x = 0; x < kStages; ++x)
+                if (__shfl_sync(0xffffffffu, stage_key, x) >= 0)
+                    wait_bounded(ring.bar0 + x * 8, (ring.phase >> x) & 1, drain);
         }
     }
 
-    // ---- join the warps
+    // ---- join the warps (the rings are idle: the buffer lies over them)
+    __syncthreads();
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -299,14 +361,12 @@ __device__ __forceinline__ void run_piece(const PagedAttnParams &P, const Item &
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             if (r == 0) sm_ml[warp * 8 * NT + t * 8 + 2 * c + i] = make_float2(st.m[t][i], l);
-            float *dst = sm_o + (size_t)(warp * 8 * NT + t * 8 + 2 * c + i) * kOPad + 8 * r;
+            float *dst = sm_o + (size_t)(warp * 8 * NT + t * 8 + 2 * c + i) * kOPad + r;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int e = 0; e < 8; e += 4)
-                    *reinterpret_cast<float4 *>(dst + hf * 64 + e) =
-                        make_float4(st.o[t][e][2 * hf + i], st.o[t][e + 1][2 * hf + i], st.o[t][e + 2][2 * hf + i],
-                                    st.o[t][e + 3][2 * hf + i]);
+            for (int m = 0; m < 8; ++m) {
+                dst[16 * m] = st.o[t][m][i];
+                dst[16 * m + 8] = st.o[t][m][2 + i];
+            }
         }
     __syncthreads();
     for (int row = warp; row < it.rows; row += kWarps) {
@@ -342,25 +402,48 @@ __device__ __forceinline__ void run_piece(const PagedAttnParams &P, const Item &
                     l == 0.f ? -INFINITY : (m - Ty::kShift + __log2f(l)) * 0.69314718055994531f;
         }
     }
-    __syncthreads();  // the buffers are free for the next piece
+    fence_proxy_async_smem();  // the buffer's accesses come before the next piece's loads
+    __syncthreads();
 }
 
-template <int NT>
-constexpr int join_bytes() {
-    return kWarps * 8 * NT * (kOPad * 4 + 8);
+// Barriers and ring of the calling warp; the whole CTA calls it.
+__device__ __forceinline__ Ring ring_init(uint8_t *smem, WaitCtl &wc, const PagedAttnParams &P) {
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kSmemBar);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + kWarps * kStages);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(bars + i), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    wc.abort_flag = abort_flag;
+    wc.status = &P.hdr->status;
+    wc.limit_ns = P.wait_limit_ns;
+    return {smem_u32(smem) + warp * kStages * kStageBytes, smem_u32(bars + warp * kStages), 0u};
 }
+
+__device__ __forceinline__ uint8_t *align_1k(uint8_t *p) {
+    return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+static_assert(kWarps * 16 * (kOPad * 4 + 8) <= kRingBytes, "the join buffer fits over the rings");
 
 // ------------------------------------------------------------------ dense
 // Work units: 16-key groups, sequence after sequence; within one, (kv-head, row
 // tile) after one another.  CTA c of C takes units [U c / C, U (c + 1) / C).
 template <class Ty, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_dense_kernel(const __grid_constant__ PagedAttnParams P) {
-    extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, 2) paged_dense_kernel(const __grid_constant__ StreamParams SP) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1k(smem_raw);
     float *sm_o = reinterpret_cast<float *>(smem);
     float2 *sm_ml = reinterpret_cast<float2 *>(smem + kWarps * 8 * NT * kOPad * 4);
-    long long *pre = reinterpret_cast<long long *>(smem + join_bytes<NT>());  // [n_seqs + 1] units before sequence s
+    long long *pre = reinterpret_cast<long long *>(smem + kSmemPre);
     __shared__ long long warp_sum[kWarps];
+    const PagedAttnParams &P = SP.a;
     const PagedSeqs &S = P.seqs;
+    WaitCtl wc;
+    Ring ring = ring_init(smem, wc, P);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const int per = (S.n_seqs + kThreads - 1) / kThreads;
@@ -450,22 +533,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_dense_kernel(
         if (!whole) slot_item[which] = id;
         // the item's first slot, for the joining kernel (-1: already whole)
         if (ga == 0 && threadIdx.x == 0) P.part_item[P.n_slots + id] = slot;
-        run_piece<Ty, NT, false>(P, it, nullptr, 0, ga, gb, slot, sm_o, sm_ml);
+        run_piece<Ty, NT, false>(SP, it, nullptr, 0, ga, gb, slot, ring, wc, sm_o, sm_ml);
         u += gb - ga;
         ++n_piece;
     }
     if (threadIdx.x < 2) P.part_item[2 * blockIdx.x + threadIdx.x] = threadIdx.x ? slot_item[1] : slot_item[0];
+    launch_dependents();
 }
 
 // ------------------------------------------------------------------ selected pages
 // One CTA per (token, kv-head, row tile) and part of its page list.
 template <class Ty, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_sparse_kernel(const __grid_constant__ PagedAttnParams P) {
-    extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, 2) paged_sparse_kernel(const __grid_constant__ StreamParams SP) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1k(smem_raw);
     float *sm_o = reinterpret_cast<float *>(smem);
     float2 *sm_ml = reinterpret_cast<float2 *>(smem + kWarps * 8 * NT * kOPad * 4);
     __shared__ int found;
+    const PagedAttnParams &P = SP.a;
     const PagedSeqs &S = P.seqs;
+    WaitCtl wc;
+    Ring ring = ring_init(smem, wc, P);
     const int part = blockIdx.x % P.parts, item = blockIdx.x / P.parts;
     const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
     const int rt = item % tiles, h = (item / tiles) % P.hkv, t = item / tiles / P.hkv;
@@ -495,8 +583,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_sparse_kernel
     if (it.pos0 < 0) cnt = 0;
     const int gp = S.page >> 4;
     const int a = (int)((long long)cnt * part / P.parts), b = (int)((long long)cnt * (part + 1) / P.parts);
-    run_piece<Ty, NT, true>(P, it, P.blk_idx + (long long)li * P.topk, cnt, a * gp, b * gp,
-                            P.parts > 1 ? item * P.parts + part : -1, sm_o, sm_ml);
+    run_piece<Ty, NT, true>(SP, it, P.blk_idx + (long long)li * P.topk, cnt, a * gp, b * gp,
+                            P.parts > 1 ? item * P.parts + part : -1, ring, wc, sm_o, sm_ml);
+    launch_dependents();
 }
 
 // ------------------------------------------------------------------ join
@@ -508,6 +597,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     const PagedSeqs &S = P.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int id = blockIdx.x, row = blockIdx.y;
+    wait_for_primary();
     int h, x, tok0, first, n_part;
     if (kSparse) {
         const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
@@ -586,37 +676,62 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
         P.lse[(size_t)tok * P.hq + hh] = l == 0.f ? -INFINITY : (m - Ty::kShift + __log2f(l)) * 0.69314718055994531f;
 }
 
-template <class Ty, int NT>
-cudaError_t launch_dense(const PagedAttnParams &P, cudaStream_t st) {
-    const PagedSeqs &S = P.seqs;
-    const int bytes = join_bytes<NT>() + (S.n_seqs + 1) * (int)sizeof(long long);
-    cudaError_t e = cudaFuncSetAttribute(paged_dense_kernel<Ty, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         join_bytes<NT>() + (kMaxSeqs + 1) * (int)sizeof(long long));
-    if (e != cudaSuccess) return e;
-    const int rt = (S.max_q * P.group + 8 * NT - 1) / (8 * NT);
-    ProfScope prof("paged_dense", st);
-    paged_dense_kernel<Ty, NT><<<kStreamGrid, kThreads, bytes, st>>>(P);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    const dim3 grid(S.n_seqs * P.hkv * rt, min(8 * NT, S.max_q * P.group));
-    paged_join_kernel<Ty, NT, false><<<grid, kThreads, 0, st>>>(P);
-    return cudaGetLastError();
+// Launches the joining kernel so that its start overlaps the end of the kernel
+// before it (it waits for that one's results itself).
+cudaError_t launch_join(void (*kernel)(PagedAttnParams), dim3 grid, const PagedAttnParams &P, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P);
 }
 
 template <class Ty, int NT>
-cudaError_t launch_sparse(const PagedAttnParams &P, cudaStream_t st) {
+cudaError_t launch_dense(const StreamParams &SP, cudaStream_t st) {
+    const PagedAttnParams &P = SP.a;
+    const PagedSeqs &S = P.seqs;
+    const int bytes = (int)kSmemPre + (S.n_seqs + 1) * (int)sizeof(long long) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(paged_dense_kernel<Ty, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmemPre + (kMaxSeqs + 1) * (int)sizeof(long long) + 1024);
+    if (e != cudaSuccess) return e;
+    const int rt = (S.max_q * P.group + 8 * NT - 1) / (8 * NT);
+    ProfScope prof("paged_dense", st);
+    paged_dense_kernel<Ty, NT><<<kStreamGrid, kThreads, bytes, st>>>(SP);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_join(paged_join_kernel<Ty, NT, false>, dim3(S.n_seqs * P.hkv * rt, min(8 * NT, S.max_q * P.group)),
+                       P, st);
+}
+
+template <class Ty, int NT>
+cudaError_t launch_sparse(const StreamParams &SP, cudaStream_t st) {
+    const PagedAttnParams &P = SP.a;
     const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
     const long long items = (long long)P.seqs.total * P.hkv * tiles;
     if (items * P.parts > 0x7fffffffll) return cudaErrorInvalidValue;
+    const int bytes = (int)kSmemPre + 1024;
     cudaError_t e = cudaFuncSetAttribute(paged_sparse_kernel<Ty, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         join_bytes<NT>());
+                                         bytes);
     if (e != cudaSuccess) return e;
     ProfScope prof("paged_sparse", st);
-    paged_sparse_kernel<Ty, NT><<<(unsigned)(items * P.parts), kThreads, join_bytes<NT>(), st>>>(P);
+    paged_sparse_kernel<Ty, NT><<<(unsigned)(items * P.parts), kThreads, bytes, st>>>(SP);
     e = cudaGetLastError();
     if (e != cudaSuccess || P.parts == 1) return e;
-    paged_join_kernel<Ty, NT, true><<<dim3((unsigned)items, min(8 * NT, P.group)), kThreads, 0, st>>>(P);
-    return cudaGetLastError();
+    return launch_join(paged_join_kernel<Ty, NT, true>, dim3((unsigned)items, min(8 * NT, P.group)), P, st);
+}
+
+cudaError_t stream_maps(StreamParams &SP, const PagedAttnParams &P, bool fp16) {
+    memset(&SP, 0, sizeof(SP));
+    SP.a = P;
+    const PagedSeqs &S = P.seqs;
+    cudaError_t e = make_tmap_pages(&SP.tmap_k, P.k, fp16, S.page, P.hkv, S.num_pages, P.kc_ps, kGroup);
+    if (e == cudaSuccess) e = make_tmap_pages(&SP.tmap_v, P.v, fp16, S.page, P.hkv, S.num_pages, P.vc_ps, kGroup);
+    return e;
 }
 
 }  // namespace
@@ -645,14 +760,20 @@ StreamPlan paged_sparse_plan(int total, int hkv, int group, int topk, int page) 
 
 cudaError_t run_paged_stream(const PagedAttnParams &P, bool fp16, int rows, cudaStream_t st) {
     if (P.seqs.n_seqs == 0 || P.seqs.total == 0) return cudaSuccess;
-    if (fp16) return rows == 8 ? launch_dense<Fp16, 1>(P, st) : launch_dense<Fp16, 2>(P, st);
-    return rows == 8 ? launch_dense<Bf16, 1>(P, st) : launch_dense<Bf16, 2>(P, st);
+    StreamParams SP;
+    const cudaError_t e = stream_maps(SP, P, fp16);
+    if (e != cudaSuccess) return e;
+    if (fp16) return rows == 8 ? launch_dense<Fp16, 1>(SP, st) : launch_dense<Fp16, 2>(SP, st);
+    return rows == 8 ? launch_dense<Bf16, 1>(SP, st) : launch_dense<Bf16, 2>(SP, st);
 }
 
 cudaError_t run_paged_sparse(const PagedAttnParams &P, bool fp16, int rows, cudaStream_t st) {
     if (P.seqs.n_seqs == 0 || P.seqs.total == 0) return cudaSuccess;
-    if (fp16) return rows == 8 ? launch_sparse<Fp16, 1>(P, st) : launch_sparse<Fp16, 2>(P, st);
-    return rows == 8 ? launch_sparse<Bf16, 1>(P, st) : launch_sparse<Bf16, 2>(P, st);
+    StreamParams SP;
+    const cudaError_t e = stream_maps(SP, P, fp16);
+    if (e != cudaSuccess) return e;
+    if (fp16) return rows == 8 ? launch_sparse<Fp16, 1>(SP, st) : launch_sparse<Fp16, 2>(SP, st);
+    return rows == 8 ? launch_sparse<Bf16, 1>(SP, st) : launch_sparse<Bf16, 2>(SP, st);
 }
 
 }  // namespace minf
