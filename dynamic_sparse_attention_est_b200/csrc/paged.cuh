@@ -137,6 +137,27 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint
         : "memory");
 }
 
+// One launch after another may start while the first still runs (its wait below);
+// the first allows it with launch_dependents.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches a kernel so that its start overlaps the end of the one before it in
+// the stream; it waits for that one's results itself (wait_for_primary).
+template <class... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, dim3 block, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ------------------------------------------------------------------ launches
 // TMA descriptors with 128-byte swizzle: any 4-D 16-bit tensor (strides in bytes),
 // and the pages of a cache, {128, P, hkv, pages} with `rows` keys x 64 channels a box.

@@ -8,19 +8,20 @@
 // 256 rows, and while the tensor cores multiply for one tile the softmax of the
 // other runs.
 //
-// Per 128x128 tile the tensor pipe needs 1,024 clocks (S = Q K^T and O += P V),
-// the 16,384 exponentials 1,024 clocks of MUFU, and shared memory about 1,000
-// clocks (operands 96 KB, the TMA's writes 32 KB per tile since two tiles share
-// them, at 128 B a clock).
+// A row tile's S has two 64-key halves that are handed over separately: while the
+// softmax works on one half, the tensor cores multiply P of the other half by V
+// and write the S of 64 keys further on over it, so neither side waits for the
+// other's latency.  (With whole 128-key tiles in turn, S -> softmax -> P V -> S is
+// one chain per row tile: 4,440 clocks for 128 keys against 256 rows.)
 //
 // Warp roles (384 threads, one persistent CTA per SM):
 //   warp 0       TMA producer: Q of a unit, then K and V tiles in turn through one
 //                ring; looks the pages up, one lane per box
-//   warp 1       TMEM allocator, tcgen05.mma issue
+//   warps 1, 2   tcgen05.mma issue of row tile 0 and 1 (warp 1 allocates TMEM)
 //   warps 4..7   softmax and output of row tile 0
 //   warps 8..11  softmax and output of row tile 1
-// TMEM columns: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P overwrites the
-// first half of its S.
+// TMEM columns: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); the P of a 64-key
+// half overwrites the first 32 columns of its S.
 //
 // Units: the key tiles of a row-tile pair are cut into parts of one length, chosen
 // by every CTA alike from the lengths on the device so that the units fill the SMs
@@ -43,18 +44,40 @@ constexpr uint32_t kTileBytes = 32768;  // 128 rows x 128 16-bit values
 constexpr uint32_t kSmemQ = 0;          // two row tiles
 constexpr uint32_t kSmemRing = 2 * kTileBytes;
 constexpr uint32_t kSmemBar = kSmemRing + kStages * kTileBytes;
-constexpr uint32_t kSmemPlan = kSmemBar + 256;  // int2 [n_seqs + 1]
+constexpr uint32_t kSmemPlan = kSmemBar + 320;  // int2 [n_seqs + 1]
 constexpr uint32_t kSmemMax = 232448;
 static_assert(kSmemPlan + 8 * (kMaxSeqs + 1) + 1024 <= kSmemMax, "the plan of kMaxSeqs sequences fits");
 // Register split after setmaxnreg: 128 x 72 + 256 x 216 = 384 x 168.
 constexpr int kRegsLaunch = 168, kRegsLoad = 72, kRegsSoftmax = 216;
 static_assert(128 * kRegsLoad + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 
-enum : int { B_Q_FULL = 0, B_Q_EMPTY = 1, B_FULL = 2, B_EMPTY = 6, B_S_FULL = 10, B_P_FULL = 12, B_O_FULL = 14,
-             B_COUNT = 16 };
+// S_FULL and P_FULL: one per row tile and 64-key half (2 t + h); O_PREV and O_FULL,
+// once a unit: O holds all steps but the last, and all of them
+enum : int { B_Q_FULL = 0, B_Q_EMPTY = 1, B_FULL = 2, B_EMPTY = 6, B_S_FULL = 10, B_P_FULL = 14, B_O_PREV = 18,
+             B_O_FULL = 20, B_COUNT = 22 };
+constexpr uint32_t kSmemWarpSum = kSmemBar + 208;  // int2 [12]
 
-constexpr uint32_t idesc(uint32_t type, bool b_mn_major) {
-    return (1u << 4) | type | ((b_mn_major ? 1u : 0u) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t idesc(uint32_t type, int n, bool b_mn_major) {
+    return (1u << 4) | type | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// O += P V for 64 keys: A = P from TMEM (8 columns per 16 keys), B = 64 rows of V
+// (2 KB per 16 keys).  The whole warp calls it, one lane issues; the first step
+// accumulates into D iff acc_first.
+__device__ __forceinline__ void umma_ts_half_warp(uint32_t d, uint32_t a_tmem, uint64_t b0, uint32_t idesc,
+                                                  uint32_t acc_first) {
+    asm volatile(
+        "{\n\t.reg .pred p, t, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 t, %3, %3;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %6, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %8, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%9], %10, %3, t;\n\t}\n" ::"r"(d),
+        "r"(a_tmem), "l"(b0), "r"(idesc), "r"(acc_first), "r"(a_tmem + 8), "l"(b0 + 128), "r"(a_tmem + 16),
+        "l"(b0 + 256), "r"(a_tmem + 24), "l"(b0 + 384)
+        : "memory");
 }
 
 struct ChunkParams {
@@ -76,8 +99,9 @@ __device__ __forceinline__ int seq_parts(int ktiles, int part_len) {
 
 // Chooses the part length: candidate i cuts the longest sequence into i + 1 parts.
 // The estimated time of a candidate is that of its rounds of units (kGrid at a
-// time) of average length, a tail of one longest unit, and two tiles' time per
-// unit for its prologue and epilogue; candidates whose cut units exceed the
+// time) of average length, a tail of one longest unit, and per unit two tiles'
+// time for its prologue and epilogue, four more for the traffic of its partial
+// result (256 KB written and read); candidates whose cut units exceed the
 // partial slots are out.  Every CTA computes the same result.
 __device__ int choose_part_len(const ChunkParams &P, int *len_sh) {
     const PagedSeqs &S = P.a.seqs;
@@ -105,7 +129,7 @@ __device__ int choose_part_len(const ChunkParams &P, int *len_sh) {
         if (cut <= P.max_slots && units > 0) {
             const float avg = work / (float)units;
             const float rounds = (float)((units + kGrid - 1) / kGrid);
-            cost = rounds * (avg + 2.f) + fmaxf(0.f, (float)len - avg);
+            cost = rounds * (avg + (cut > 0 ? 6.f : 2.f)) + fmaxf(0.f, (float)len - avg);
         }
         float best = cost;
 #pragma unroll
@@ -169,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + B_COUNT);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + B_COUNT + 1);
     int *len_sh = reinterpret_cast<int *>(bars + B_COUNT + 2);
-    int2 *warp_sum = reinterpret_cast<int2 *>(bars + B_COUNT + 3);  // [12]
+    int2 *warp_sum = reinterpret_cast<int2 *>(smem + kSmemWarpSum);
     int2 *pre = reinterpret_cast<int2 *>(smem + kSmemPlan);
     auto bar = [&](int i) { return smem_u32(bars + i); };
     const PagedSeqs &S = P.a.seqs;
@@ -177,15 +201,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 
     if (threadIdx.x == 0) {
         mbar_init(bar(B_Q_FULL), 1);
-        mbar_init(bar(B_Q_EMPTY), 1);
+        mbar_init(bar(B_Q_EMPTY), 2);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(bar(B_FULL + s), 1);
-            mbar_init(bar(B_EMPTY + s), 1);
+            mbar_init(bar(B_EMPTY + s), 2);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 4; ++b) {
             mbar_init(bar(B_S_FULL + b), 1);
             mbar_init(bar(B_P_FULL + b), 128);
-            mbar_init(bar(B_O_FULL + b), 1);
+            mbar_init(bar(B_O_PREV + b), 1);  // B_O_FULL follows it
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -245,9 +269,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     __syncthreads();
     tc_fence_after();
     const int n_units = pre[S.n_seqs].x;
-    if (blockIdx.x == 0) {  // the joining kernel's copy of the plan
-        for (int s = threadIdx.x; s <= S.n_seqs; s += kThreads) P.a.part_item[1 + s] = pre[s].y;
-        if (threadIdx.x == 0) P.a.part_item[0] = part_len;
+    if (blockIdx.x == 0 && warp == 3) {  // the joining kernel's copy: (slots, pairs) cut before each sequence
+        int2 *dst = reinterpret_cast<int2 *>(P.a.part_item + 2);
+        int cut = 0;
+        for (int s0 = 0; s0 <= S.n_seqs; s0 += 32) {
+            const int s = s0 + lane;
+            int mine = 0;
+            if (s < S.n_seqs && pre[s + 1].y > pre[s].y) {
+                const SeqView v = seq_view(S, s, P.a.hdr);
+                mine = P.a.hkv * seq_pairs(v, P.tpt);
+            }
+            int inc = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            if (s <= S.n_seqs) dst[s] = make_int2(pre[s].y, cut + inc - mine);
+            cut += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) P.a.part_item[0] = part_len;
     }
     const uint32_t tmem = *tmem_slot;
     const WaitCtl wc{abort_flag, &P.a.hdr->status, P.a.wait_limit_ns};
@@ -270,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 const Unit n = unit_at(P, pre, part_len, u);
                 if (n.ka >= n.kb) continue;
                 int pg = page_for(n, n.ka);
-                ok = __all_sync(0xffffffffu, wait_bounded(bar(B_Q_EMPTY), (n_q & 1) ^ 1, wc, wait_site(1, B_Q_EMPTY, u)));
+                ok = __all_sync(0xffffffffu, wait_bounded_sleep(bar(B_Q_EMPTY), (n_q & 1) ^ 1, wc, wait_site(1, B_Q_EMPTY, u)));
                 if (!ok) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar(B_Q_FULL), n.two ? 2 * q_bytes : q_bytes);
@@ -285,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     const int n_load = __popc(__ballot_sync(0xffffffffu, pg >= 0));
                     for (int kv = 0; kv < 2; ++kv) {
                         const int st = fill % kStages;
-                        ok = __all_sync(0xffffffffu, wait_bounded(bar(B_EMPTY + st), ((fill / kStages) & 1) ^ 1, wc,
+                        ok = __all_sync(0xffffffffu, wait_bounded_sleep(bar(B_EMPTY + st), ((fill / kStages) & 1) ^ 1, wc,
                                                                   wait_site(1, B_EMPTY + st, j)));
                         if (!ok) break;
                         if (lane == 0) mbar_arrive_expect_tx(bar(B_FULL + st), (uint32_t)(n_load * box * 128));
@@ -305,53 +346,79 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 volatile int no_abort = 0;
                 const WaitCtl drain{&no_abort, nullptr, 50000000ull};
                 for (int f = max(0, fill - kStages); f < fill; ++f)
-                    wait_bounded(bar(B_FULL + f % kStages), (f / kStages) & 1, drain);
-                if (n_q > 0) wait_bounded(bar(B_Q_FULL), (n_q - 1) & 1, drain);
+                    wait_bounded_sleep(bar(B_FULL + f % kStages), (f / kStages) & 1, drain);
+                if (n_q > 0) wait_bounded_sleep(bar(B_Q_FULL), (n_q - 1) & 1, drain);
             }
-        } else if (warp == 1) {
+        } else if (warp < 3) {
             // ------------------------------------------------------ MMA issue (whole warp; one lane issues)
-            constexpr uint32_t kQK = idesc(Ty::kIdescType, false), kPV = idesc(Ty::kIdescType, true);
+            // One warp per row tile: an instruction takes its issuer about as long as the
+            // tensor pipe, so a single warp would be the bound.
+            // Step i is 64 keys (half h = i & 1 of key tile i / 2).  S_t(i + 2) goes out
+            // after P_t(i) V(i), which the tensor pipe finishes first, so P is consumed
+            // before S overwrites it; the barrier of S_t(i + 2) also says that O holds the
+            // steps up to i.
+            constexpr uint32_t kQK = idesc(Ty::kIdescType, 64, false), kPV = idesc(Ty::kIdescType, 128, true);
             const uint64_t dq = sdesc_sw128(sQ, 16, 1024), dk = sdesc_sw128(sR, 16, 1024);
             const uint64_t dv = sdesc_sw128(sR, 16384, 1024);
-            int used = 0, n_q = 0;           // ring stages taken (K then V per key tile), Q loads seen
-            int np[2] = {0, 0};              // P tiles seen per row tile
+            const int t = warp - 1;  // row tile
+            int used = 0, n_q = 0;   // ring stages taken (K then V per key tile), Q loads seen
+            uint32_t pp = 0;         // parity of the next P of each half
             bool ok = true;
             auto wait_full = [&](int f, int site) -> bool {
-                return __all_sync(0xffffffffu, wait_bounded(bar(B_FULL + f % kStages), (f / kStages) & 1, wc, site));
+                return __all_sync(0xffffffffu, wait_bounded_sleep(bar(B_FULL + f % kStages), (f / kStages) & 1, wc, site));
             };
-            auto issue_s = [&](int t, int f) {
-                umma_ss_tile_warp(tmem + t * 128, dq + (uint64_t)((t * kTileBytes) >> 4),
-                                  dk + (uint64_t)(((f % kStages) * kTileBytes) >> 4), kQK, 0u);
-                umma_commit_warp(bar(B_S_FULL + t));
+            auto issue_s = [&](int h, int f) {
+                umma_ss_tile_warp(tmem + t * 128 + h * 64, dq + (uint64_t)((t * kTileBytes) >> 4),
+                                  dk + (uint64_t)(((f % kStages) * kTileBytes + h * 8192) >> 4), kQK, 0u);
             };
             for (int u = blockIdx.x; ok && u < n_units; u += gridDim.x) {
                 const Unit n = unit_at(P, pre, part_len, u);
-                const int T = n.kb - n.ka, nt = n.two ? 2 : 1;
+                const int T = n.kb - n.ka;
                 if (T <= 0) continue;
-                ok = __all_sync(0xffffffffu, wait_bounded(bar(B_Q_FULL), n_q & 1, wc, wait_site(3, B_Q_FULL, u)));
+                if (t == 1 && !n.two) {
+                    // Nothing to multiply, but every stage is taken and given back: a warp that
+                    // ran ahead of the ring would take an older phase's parity for its own.
+                    ok = __all_sync(0xffffffffu, wait_bounded_sleep(bar(B_Q_FULL), n_q & 1, wc, wait_site(3, B_Q_FULL, u)));
+                    if (!ok) break;
+                    ++n_q;
+                    if (lane == 0) mbar_arrive(bar(B_Q_EMPTY));
+                    for (int x = 0; ok && x < 2 * T; ++x, ++used) {
+                        ok = wait_full(used, wait_site(3, B_FULL + 3, x));
+                        if (ok && lane == 0) mbar_arrive(bar(B_EMPTY + used % kStages));
+                    }
+                    continue;
+                }
+                ok = __all_sync(0xffffffffu, wait_bounded_sleep(bar(B_Q_FULL), n_q & 1, wc, wait_site(3, B_Q_FULL, u)));
                 if (!ok || !(ok = wait_full(used, wait_site(3, B_FULL, 0)))) break;
                 ++n_q;
                 tc_fence_after();
-                for (int t = 0; t < nt; ++t) issue_s(t, used);
+                for (int h = 0; h < 2; ++h) {
+                    issue_s(h, used);
+                    umma_commit_warp(bar(B_S_FULL + 2 * t + h));
+                }
                 umma_commit_warp(bar(B_EMPTY + used % kStages));
                 if (T == 1) umma_commit_warp(bar(B_Q_EMPTY));
                 for (int j = 0; ok && j < T; ++j) {
                     const int fv = used + 1, fk = used + 2;  // this tile's V, the next tile's K
-                    for (int t = 0; ok && t < nt; ++t) {
-                        ok = __all_sync(0xffffffffu, wait_bounded(bar(B_P_FULL + t), np[t] & 1, wc,
-                                                                  wait_site(3, B_P_FULL + t, j)));
+                    const bool more = j + 1 < T;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int b = 2 * t + h;
+                        ok = __all_sync(0xffffffffu, wait_bounded_sleep(bar(B_P_FULL + b), (pp >> h) & 1, wc,
+                                                                  wait_site(3, B_P_FULL + b, j)));
                         if (!ok) break;
-                        ++np[t];
-                        if (t == 0) {
+                        pp ^= 1u << h;
+                        if (h == 0) {
                             if (!(ok = wait_full(fv, wait_site(3, B_FULL + 1, j)))) break;
                             const int valid = n.len - (n.ka + j) * kKeyTile;
                             if (valid < kKeyTile) {
                                 // rows behind the stored tokens: whatever they hold, 0 * it must be 0
+                                // (both warps write the same zeros)
                                 const uint32_t st = sR + (fv % kStages) * kTileBytes;
                                 for (int i = valid * 8 + lane; i < kKeyTile * 8; i += 32)
 #pragma unroll
-                                    for (int x = 0; x < 2; ++x)
-                                        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(st + x * 16384 + i * 16),
+                                    for (int y = 0; y < 2; ++y)
+                                        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(st + y * 16384 + i * 16),
                                                      "r"(0u)
                                                      : "memory");
                                 fence_proxy_async_smem();
@@ -359,20 +426,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                             }
                         }
                         tc_fence_after();
-                        umma_ts_tile_warp(tmem + 256 + t * 128, tmem + t * 128,
-                                          dv + (uint64_t)(((fv % kStages) * kTileBytes) >> 4), kPV, j > 0 ? 1u : 0u);
-                        if (t == nt - 1) umma_commit_warp(bar(B_EMPTY + fv % kStages));
-                        if (j + 1 < T) {
-                            if (t == 0 && !(ok = wait_full(fk, wait_site(3, B_FULL + 2, j)))) break;
-                            tc_fence_after();
-                            issue_s(t, fk);
-                            if (t == nt - 1) {
-                                umma_commit_warp(bar(B_EMPTY + fk % kStages));
-                                if (j + 2 == T) umma_commit_warp(bar(B_Q_EMPTY));  // the unit's last use of Q
+                        umma_ts_half_warp(tmem + 256 + t * 128, tmem + t * 128 + h * 64,
+                                          dv + (uint64_t)(((fv % kStages) * kTileBytes + h * 8192) >> 4), kPV,
+                                          j > 0 || h > 0 ? 1u : 0u);
+                        if (more) {
+                            if (h == 0) {
+                                if (!(ok = wait_full(fk, wait_site(3, B_FULL + 2, j)))) break;
+                                tc_fence_after();
                             }
-                        } else {
-                            umma_commit_warp(bar(B_O_FULL + t));
+                            issue_s(h, fk);
                         }
+                        umma_commit_warp(bar(more ? B_S_FULL + b : (h == 0 ? B_O_PREV : B_O_FULL) + t));
+                    }
+                    if (!ok) break;
+                    umma_commit_warp(bar(B_EMPTY + fv % kStages));  // free when both row tiles are done
+                    if (more) {
+                        umma_commit_warp(bar(B_EMPTY + fk % kStages));
+                        if (j + 2 == T) umma_commit_warp(bar(B_Q_EMPTY));  // the unit's last use of Q
                     }
                     used += 2;
                 }
@@ -388,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         const uint32_t tO = tmem + lane_off + 256 + t * 128;
         const float sl2 = P.a.scale_log2;
         const int G = P.a.group;
-        int ns = 0, no = 0;  // S tiles and outputs seen
+        uint32_t sp = 0, op = 0;  // parity of the next S of each half, and of the unit's O
         bool ok = true;
         for (int u = blockIdx.x; ok && u < n_units; u += gridDim.x) {
             const Unit n = unit_at(P, pre, part_len, u);
@@ -399,23 +469,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             const int pos = n.pos0 + n.tok0 + t * P.tpt + min(r / G, n_here - 1);
             const int pos_min = n.pos0 + n.tok0 + t * P.tpt;
             float m_run = -INFINITY, l_run = 0.f;
-            for (int j = n.ka; j < n.kb; ++j) {
-                const bool got = wait_bounded(bar(B_S_FULL + t), ns & 1, wc, wait_site(4 + t, B_S_FULL + t, j));
+            const int i0 = 2 * n.ka, i1 = 2 * n.kb;
+            for (int i = i0; i < i1; ++i) {
+                const int h = i & 1;
+                const uint32_t tSh = tS + h * 64;
+                const bool got = wait_bounded_sleep(bar(B_S_FULL + 2 * t + h), (sp >> h) & 1, wc,
+                                              wait_site(4 + t, B_S_FULL + 2 * t + h, i));
                 if (__any_sync(0xffffffffu, !got)) {  // tcgen05.ld below is warp-wide
                     ok = false;
                     break;
                 }
-                ++ns;
+                sp ^= 1u << h;
                 tc_fence_after();
-                uint32_t sr[4][32];
+                uint32_t sr[2][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
+                for (int c = 0; c < 2; ++c) tmem_ld32(tSh + c * 32, sr[c]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
-                if (pos_min + 1 < (j + 1) * kKeyTile) {  // the diagonal or the end crosses this tile
-                    const int vis = pos + 1 - j * kKeyTile;
+                for (int c = 0; c < 2; ++c) tmem_ld_wait(sr[c]);
+                if (pos_min + 1 < (i + 1) * 64) {  // the diagonal or the end crosses these keys
+                    const int vis = pos + 1 - i * 64;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (c * 32 + e >= vis) sr[c][e] = 0xff800000u;  // -inf
@@ -424,16 +498,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 float mc[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    mc[c] = fmaxf(__uint_as_float(sr[c][0]), __uint_as_float(sr[c][1]));
+                    const uint32_t *x = &sr[c >> 1][(c & 1) * 16];
+                    mc[c] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
-                    for (int e = 2; e < 32; e += 2)
-                        mc[c] = fmax3(mc[c], __uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1]));
+                    for (int e = 2; e < 16; e += 2)
+                        mc[c] = fmax3(mc[c], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                 }
                 const float m_new = fmaxf(m_run, fmax3(mc[0], mc[1], fmaxf(mc[2], mc[3])) * sl2);
                 const bool want = m_new > m_run + Ty::kLag;  // includes m_run = -inf with a finite m_new
                 const float alpha = want ? ex2_approx(m_run - m_new) : 1.f;
-                // the P V of the tiles before is complete (S of this tile was issued after it)
-                if (j > n.ka && __any_sync(0xffffffffu, want && m_run != -INFINITY)) {
+                if (i > i0 && __any_sync(0xffffffffu, want && m_run != -INFINITY)) {
+                    // O must hold the steps before this one: the next step's S was issued after them
+                    const int next = i + 1 < i1 ? B_S_FULL + 2 * t + (h ^ 1) : B_O_PREV + t;
+                    const bool done = wait_bounded_sleep(bar(next), i + 1 < i1 ? (sp >> (h ^ 1)) & 1 : op, wc,
+                                                         wait_site(6, next, i));
+                    if (__any_sync(0xffffffffu, !done)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t o[32];
@@ -451,9 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 const float m_use = m_run == -INFINITY ? 0.f : m_run - Ty::kShift;
                 const uint64_t sl2x2 = f32x2_splat(sl2), negm = f32x2_splat(-m_use);
                 uint64_t acc0 = 0, acc1 = 0;
-                uint32_t pp[2][32];
+                uint32_t pk[32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const uint64_t x = f32x2_fma(
@@ -466,26 +549,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                         else acc0 = f32x2_add(acc0, f32x2_pack(p0, p1));
                         // P is rounded to the cache's type for the product (the size of the
                         // output's own rounding); the sum keeps fp32
-                        pp[c >> 1][(c & 1) * 16 + e] = Ty::pack(p0, p1);
+                        pk[c * 16 + e] = Ty::pack(p0, p1);
                     }
-                    if (c == 1) tmem_st32(tS, pp[0]);
                 }
+                tmem_st32(tSh, pk);
                 float a0, a1, b0, b1;
                 f32x2_unpack(acc0, a0, a1);
                 f32x2_unpack(acc1, b0, b1);
                 l_run += (a0 + a1) + (b0 + b1);
-                tmem_st32(tS + 32, pp[1]);
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(bar(B_P_FULL + t));
+                mbar_arrive(bar(B_P_FULL + 2 * t + h));
             }
             if (!ok) break;
             // -------------------------------------------------------- output
             const bool any = n.kb > n.ka;
             if (any) {
-                const bool got = wait_bounded(bar(B_O_FULL + t), no & 1, wc, wait_site(4 + t, B_O_FULL + t, u));
+                const bool got = wait_bounded_sleep(bar(B_O_FULL + t), op, wc, wait_site(4 + t, B_O_FULL + t, u));
                 if (__any_sync(0xffffffffu, !got)) break;
-                ++no;
+                op ^= 1u;
                 tc_fence_after();
             }
             const int hh = n.h * G + r % G;
@@ -533,65 +615,66 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    launch_dependents();
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------ join
-// One warp per row of a cut pair: its parts in order.
+// One CTA per 32 rows of a cut pair at a time, one warp per row: its parts in order.
+constexpr int kJoinRows = 32;
 template <class Ty>
-__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const __grid_constant__ PagedAttnParams P, int tpt,
+__global__ void __launch_bounds__(256, 5) paged_chunk_join_kernel(const __grid_constant__ PagedAttnParams P, int tpt,
                                                                int part_rows) {
     const PagedSeqs &S = P.seqs;
-    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    wait_for_primary();
     const int part_len = P.part_item[0];
-    const int *pre = P.part_item + 1;  // partial slots before each sequence
-    const int n_slots = pre[S.n_seqs];
-    const int step = gridDim.x * (blockDim.x >> 5);
-    const long long rows = (long long)n_slots * part_rows;
-    for (long long w = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < rows; w += step) {
-        const int slot = (int)(w / part_rows), r = (int)(w % part_rows);
+    const int2 *pre = reinterpret_cast<const int2 *>(P.part_item + 2);  // (slots, pairs) cut before each sequence
+    const int n_pairs = pre[S.n_seqs].y;
+    const int per = part_rows / kJoinRows;
+    for (int w = blockIdx.x; w < n_pairs * per; w += gridDim.x) {
+        const int item = w / per;
         int lo = 0, hi = S.n_seqs;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (pre[mid] <= slot) lo = mid;
+            if (pre[mid].y <= item) lo = mid;
             else hi = mid;
         }
         const SeqView v = seq_view(S, lo, P.hdr);
         const int pairs = seq_pairs(v, tpt), parts = seq_parts(seq_ktiles(v), part_len);
-        const int rem = slot - pre[lo];
-        if ((rem / pairs) % parts != 0) continue;  // the first part's warp joins them all
-        const int pair = pairs - 1 - rem % pairs, h = rem / pairs / parts;
-        const int t = r >> 7, x = (r & 127) / P.group;
-        const int tok = pair * 2 * tpt + t * tpt + x;
-        if (x >= tpt || tok >= v.n) continue;
-        float m = -INFINITY;
-        for (int i = lane; i < parts; i += 32)
-            m = fmaxf(m, P.part_ml[(size_t)(slot + i * pairs) * part_rows + r].x);
+        const int rem = item - pre[lo].y, h = rem / pairs, at = rem % pairs;
+        const size_t slot0 = (size_t)pre[lo].x + (size_t)h * parts * pairs + at;  // part i: pairs further on
+        for (int x = warp; x < kJoinRows; x += 8) {
+            const int r = (w % per) * kJoinRows + x, in = (r & 127) / P.group;
+            const int tok = ((pairs - 1 - at) * 2 + (r >> 7)) * tpt + in;
+            if (in >= tpt || tok >= v.n) continue;
+            float m = -INFINITY;
+            for (int i = lane; i < parts; i += 32) m = fmaxf(m, P.part_ml[(slot0 + (size_t)i * pairs) * part_rows + r].x);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const size_t row = (size_t)(slot + i * pairs) * part_rows + r;
-            const float2 ml = P.part_ml[row];
-            const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (ml.y != 0.f) o = reinterpret_cast<const float4 *>(P.part_o)[row * 32 + lane];
-            l = fmaf(ml.y, a, l);
-            acc.x = fmaf(o.x, a, acc.x);
-            acc.y = fmaf(o.y, a, acc.y);
-            acc.z = fmaf(o.z, a, acc.z);
-            acc.w = fmaf(o.w, a, acc.w);
+            for (int i = 0; i < parts; ++i) {
+                const size_t row = (slot0 + (size_t)i * pairs) * part_rows + r;
+                const float2 ml = P.part_ml[row];
+                const float4 o = reinterpret_cast<const float4 *>(P.part_o)[row * 32 + lane];
+                const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+                l = fmaf(ml.y, a, l);
+                acc.x = fmaf(o.x, a, acc.x);
+                acc.y = fmaf(o.y, a, acc.y);
+                acc.z = fmaf(o.z, a, acc.z);
+                acc.w = fmaf(o.w, a, acc.w);
+            }
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+            const int hh = h * P.group + (r & 127) % P.group;
+            uint2 *dst = reinterpret_cast<uint2 *>(static_cast<typename Ty::T *>(P.out) +
+                                                   (long long)(v.q0 + tok) * P.o_ts + (long long)hh * P.o_hs) + lane;
+            *dst = make_uint2(Ty::pack(acc.x * inv, acc.y * inv), Ty::pack(acc.z * inv, acc.w * inv));
+            if (lane == 0 && P.lse)
+                P.lse[(size_t)(v.q0 + tok) * P.hq + hh] =
+                    l == 0.f ? -INFINITY : (m - Ty::kShift + __log2f(l)) * 0.69314718055994531f;
         }
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        const int hh = h * P.group + (r & 127) % P.group;
-        uint2 *dst = reinterpret_cast<uint2 *>(static_cast<typename Ty::T *>(P.out) +
-                                               (long long)(v.q0 + tok) * P.o_ts + (long long)hh * P.o_hs) + lane;
-        *dst = make_uint2(Ty::pack(acc.x * inv, acc.y * inv), Ty::pack(acc.z * inv, acc.w * inv));
-        if (lane == 0 && P.lse)
-            P.lse[(size_t)(v.q0 + tok) * P.hq + hh] =
-                l == 0.f ? -INFINITY : (m - Ty::kShift + __log2f(l)) * 0.69314718055994531f;
     }
 }
 
@@ -612,8 +695,7 @@ cudaError_t launch_chunk(const ChunkParams &C, cudaStream_t st) {
     paged_chunk_kernel<Ty><<<kGrid, kThreads, bytes, st>>>(C);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    paged_chunk_join_kernel<Ty><<<2 * kGrid, 256, 0, st>>>(C.a, C.tpt, C.part_rows);
-    return cudaGetLastError();
+    return launch_after(paged_chunk_join_kernel<Ty>, dim3(8 * kGrid), dim3(256), st, C.a, C.tpt, C.part_rows);
 }
 
 }  // namespace
@@ -622,7 +704,7 @@ ChunkPlan paged_chunk_plan(int n_seqs, int group, int max_q) {
     ChunkPlan p{};
     p.part_rows = max_q <= 128 / group ? 128 : 256;
     p.n_slots = 8 * kGrid;
-    p.n_items = 2 + n_seqs;
+    p.n_items = 2 + 2 * (n_seqs + 1);
     return p;
 }
 

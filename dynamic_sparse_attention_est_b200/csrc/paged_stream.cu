@@ -67,11 +67,6 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                  : "r"(addr)
                  : "memory");
 }
-// One launch after another may start while the first still runs (its wait below);
-// the first allows it with launch_dependents.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // The pages a warp walks: 32 (logical block, page) entries at a time, one per
 // lane, the next 32 already loaded.
 template <bool kSparse>
@@ -676,21 +671,6 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
         P.lse[(size_t)tok * P.hq + hh] = l == 0.f ? -INFINITY : (m - Ty::kShift + __log2f(l)) * 0.69314718055994531f;
 }
 
-// Launches the joining kernel so that its start overlaps the end of the kernel
-// before it (it waits for that one's results itself).
-cudaError_t launch_join(void (*kernel)(PagedAttnParams), dim3 grid, const PagedAttnParams &P, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, P);
-}
-
 template <class Ty, int NT>
 cudaError_t launch_dense(const StreamParams &SP, cudaStream_t st) {
     const PagedAttnParams &P = SP.a;
@@ -704,8 +684,8 @@ cudaError_t launch_dense(const StreamParams &SP, cudaStream_t st) {
     paged_dense_kernel<Ty, NT><<<kStreamGrid, kThreads, bytes, st>>>(SP);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_join(paged_join_kernel<Ty, NT, false>, dim3(S.n_seqs * P.hkv * rt, min(8 * NT, S.max_q * P.group)),
-                       P, st);
+    return launch_after(paged_join_kernel<Ty, NT, false>,
+                        dim3(S.n_seqs * P.hkv * rt, min(8 * NT, S.max_q * P.group)), dim3(kThreads), st, P);
 }
 
 template <class Ty, int NT>
@@ -722,7 +702,8 @@ cudaError_t launch_sparse(const StreamParams &SP, cudaStream_t st) {
     paged_sparse_kernel<Ty, NT><<<(unsigned)(items * P.parts), kThreads, bytes, st>>>(SP);
     e = cudaGetLastError();
     if (e != cudaSuccess || P.parts == 1) return e;
-    return launch_join(paged_join_kernel<Ty, NT, true>, dim3((unsigned)items, min(8 * NT, P.group)), P, st);
+    return launch_after(paged_join_kernel<Ty, NT, true>, dim3((unsigned)items, min(8 * NT, P.group)), dim3(kThreads),
+                        st, P);
 }
 
 cudaError_t stream_maps(StreamParams &SP, const PagedAttnParams &P, bool fp16) {

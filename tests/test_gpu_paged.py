@@ -234,3 +234,16 @@ def test_chunk(lens, kv, hq, hkv, page, dtype):
     assert minf.minf_status(ws) == 0
     ref.check(c, got, ref.attention(c, SCALE))
     assert (out[sum(lens):] == 9.0).all()
+
+
+def test_chunk_many_units_of_one_and_two_row_tiles():
+    """Several units to a CTA, pairs of row tiles and single ones in every order."""
+    g = torch.Generator().manual_seed(7)
+    lens = torch.randint(1, 90, (70,), generator=g).tolist()
+    lens = [1 if i % 3 == 1 else n for i, n in enumerate(lens)]
+    kv = [n + int(x) for n, x in zip(lens, torch.randint(0, 400, (70,), generator=g))]
+    c = ref.Case(lens, kv, 16, 8, 16, HF, seed=11)
+    ws = minf.workspace(minf.paged_workspace_bytes(minf.OP_PAGED_ATTENTION, 16, 8, c.total, 70, c.max_q), c.dev)
+    got = minf.minf_paged_attention(c.q, c.k_cache, c.v_cache, *c.meta(), scale=SCALE, ws=ws)
+    assert minf.minf_status(ws) == 0
+    ref.check(c, got, ref.attention(c, SCALE))
