@@ -137,6 +137,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint
         : "memory");
 }
 
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
 // One launch after another may start while the first still runs (its wait below);
 // the first allows it with launch_dependents.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -145,10 +157,11 @@ __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontro
 // Launches a kernel so that its start overlaps the end of the one before it in
 // the stream; it waits for that one's results itself (wait_for_primary).
 template <class... A>
-cudaError_t launch_after(void (*kernel)(A...), dim3 grid, dim3 block, cudaStream_t st, A... args) {
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -224,16 +237,17 @@ struct EstimateParams {
     int hq, hkv, group, topk;
     int *blk_idx, *blk_cnt;  // [total][hkv][topk], [total][hkv]
     float *scores;           // [batch][hkv][score_stride]
-    float *top;              // [n_seqs][hkv][top_stride] largest |bound| of 16 pages
-    int score_stride, top_stride, batch;
-    int t0, t1, tiles, pages_per_cta;  // per launch
+    float *top;              // [n_seqs * tiles][hkv][ranges] largest |bound| of a tile's page range
+    int score_stride, batch;
+    int t0, t1, tiles, tile_tokens, pages_per_cta, ranges;  // per launch
     WsHeader *hdr;
+    unsigned long long wait_limit_ns;
 };
 struct EstimatePlan {
-    int score_stride, top_stride, batch;  // batch: tokens scored at a time
+    int score_stride, batch;  // batch: tokens scored at a time
     size_t n_scores, n_top;
 };
-EstimatePlan paged_estimate_plan(int total, int n_seqs, int hkv, int width);
+EstimatePlan paged_estimate_plan(int total, int n_seqs, int max_q, int hkv, int width);
 cudaError_t run_paged_estimate(const EstimateParams &P, bool fp16, cudaStream_t st);
 
 }  // namespace minf

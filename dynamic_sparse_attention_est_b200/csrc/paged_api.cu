@@ -227,7 +227,7 @@ size_t minf_paged_workspace_bytes(int op, int hq, int hkv, int total, int n_seqs
         return dense_sizes(n_seqs, hkv, hq / hkv, max_q).total;
     case MINF_OP_PAGED_BLOCK_ESTIMATE:
         if (topk < 1 || width < 1 || width > kMaxBlocks) return 0;
-        return estimate_bytes(paged_estimate_plan(total, n_seqs, hkv, width), nullptr);
+        return estimate_bytes(paged_estimate_plan(total, n_seqs, max_q, hkv, width), nullptr);
     case MINF_OP_PAGED_BLOCK_ATTENTION:
         if (topk < 1) return 0;
         return sparse_sizes(total, hkv, hq / hkv, topk, 128).total;  // the largest pages make the most parts
@@ -331,7 +331,7 @@ int minf_paged_block_estimate(const minf_paged_seqs *seqs, int dtype, int hq, in
     if ((rc = check_rows(q, "q", S.total, hq, false))) return rc;
     if (!k_bounds || !aligned16(k_bounds)) return bad(MINF_ERR_INVALID, "null or unaligned k_bounds");
     if (!blk_idx || !blk_cnt) return bad(MINF_ERR_INVALID, "null blk_idx or blk_cnt");
-    const EstimatePlan p = paged_estimate_plan(S.total, S.n_seqs, hkv, S.width);
+    const EstimatePlan p = paged_estimate_plan(S.total, S.n_seqs, S.max_q, hkv, S.width);
     size_t top_at = 0;
     if ((rc = api_check_ws(ws, ws_bytes, estimate_bytes(p, &top_at)))) return rc;
     P.q = q->data;
@@ -347,9 +347,9 @@ int minf_paged_block_estimate(const minf_paged_seqs *seqs, int dtype, int hq, in
     P.scores = reinterpret_cast<float *>(static_cast<char *>(ws) + MINF_STATUS_BYTES);
     P.top = reinterpret_cast<float *>(static_cast<char *>(ws) + top_at);
     P.score_stride = p.score_stride;
-    P.top_stride = p.top_stride;
     P.batch = p.batch;
     P.hdr = static_cast<WsHeader *>(ws);
+    P.wait_limit_ns = api_wait_limit_ns();
     const DeviceScope scope;
     if ((rc = api_select_device(k_bounds))) return rc;
     return launch_result(run_paged_estimate(P, dtype == MINF_FP16, (cudaStream_t)stream), "paged estimate launch");

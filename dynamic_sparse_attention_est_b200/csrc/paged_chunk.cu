@@ -695,7 +695,7 @@ cudaError_t launch_chunk(const ChunkParams &C, cudaStream_t st) {
     paged_chunk_kernel<Ty><<<kGrid, kThreads, bytes, st>>>(C);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_after(paged_chunk_join_kernel<Ty>, dim3(8 * kGrid), dim3(256), st, C.a, C.tpt, C.part_rows);
+    return launch_after(paged_chunk_join_kernel<Ty>, dim3(8 * kGrid), dim3(256), 0, st, C.a, C.tpt, C.part_rows);
 }
 
 }  // namespace

@@ -55,18 +55,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
 // The pages a warp walks: 32 (logical block, page) entries at a time, one per
 // lane, the next 32 already loaded.
 template <bool kSparse>
@@ -685,7 +673,7 @@ cudaError_t launch_dense(const StreamParams &SP, cudaStream_t st) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_after(paged_join_kernel<Ty, NT, false>,
-                        dim3(S.n_seqs * P.hkv * rt, min(8 * NT, S.max_q * P.group)), dim3(kThreads), st, P);
+                        dim3(S.n_seqs * P.hkv * rt, min(8 * NT, S.max_q * P.group)), dim3(kThreads), 0, st, P);
 }
 
 template <class Ty, int NT>
@@ -702,7 +690,7 @@ cudaError_t launch_sparse(const StreamParams &SP, cudaStream_t st) {
     paged_sparse_kernel<Ty, NT><<<(unsigned)(items * P.parts), kThreads, bytes, st>>>(SP);
     e = cudaGetLastError();
     if (e != cudaSuccess || P.parts == 1) return e;
-    return launch_after(paged_join_kernel<Ty, NT, true>, dim3((unsigned)items, min(8 * NT, P.group)), dim3(kThreads),
+    return launch_after(paged_join_kernel<Ty, NT, true>, dim3((unsigned)items, min(8 * NT, P.group)), dim3(kThreads), 0,
                         st, P);
 }
 

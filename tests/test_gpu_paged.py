@@ -247,3 +247,26 @@ def test_chunk_many_units_of_one_and_two_row_tiles():
     got = minf.minf_paged_attention(c.q, c.k_cache, c.v_cache, *c.meta(), scale=SCALE, ws=ws)
     assert minf.minf_status(ws) == 0
     ref.check(c, got, ref.attention(c, SCALE))
+
+
+def test_block_estimate_tiles_of_a_chunk_agree_on_the_largest_bound():
+    """Tiles of one sequence end at different pages of a 16-page step; the last page of the
+    step holds by far the largest bounds, which the later tiles' error bound must cover."""
+    c = ref.Case([200], [200 + 16 * 20], 4, 2, 16, BF, seed=2)
+    kb = ref.bounds(c)
+    pages = c.tables[0, :32].long()
+    kb[pages[27], :, 1] *= 50
+    kb = torch.nan_to_num(kb)
+    idx, cnt = minf.minf_paged_block_estimate(c.q, kb, *c.meta(), page_size=16, topk=9)
+    wi, wc = ref.estimate(c, kb, 9)
+    assert torch.equal(cnt, wc) and torch.equal(idx, wi)
+
+
+def test_block_estimate_many_rows_and_long_rows():
+    """A warp per row (many rows of at most 2,048 pages), and a CTA per row beyond."""
+    for lens, kv, page in (([350, 250], [9000, 5000], 16), ([140], [16 * 2500], 16)):
+        c = ref.Case(lens, kv, 4, 2, page, BF, seed=5)
+        kb = torch.nan_to_num(ref.bounds(c))
+        idx, cnt = minf.minf_paged_block_estimate(c.q, kb, *c.meta(), page_size=page, topk=33)
+        wi, wc = ref.estimate(c, kb, 33)
+        assert torch.equal(cnt, wc) and torch.equal(idx, wi)
