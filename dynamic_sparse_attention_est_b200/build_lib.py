@@ -1,4 +1,5 @@
-"""Builds libminf.so (the sm_100a kernels and the C ABI) in-tree with nvcc.
+"""Builds libminf.so (the sm_100a kernels and the C ABI) in-tree with nvcc, and
+_paged.so (the torch binding of the paged calls) with g++.
 
     python -m dynamic_sparse_attention_est_b200.build_lib [--force]
 """
@@ -14,6 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libminf.so")
+BINDING = os.path.join(PKG, "_paged.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -34,17 +36,39 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def build_binding() -> str:
+    """Compiles the extension module against this interpreter's torch and links it to libminf.so."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "/usr/local/cuda/include", sysconfig.get_paths()["include"], INCLUDE]
+    tmp = f"{BINDING}.{os.getpid()}.tmp"
+    cmd = ["g++", "-O2", "-fPIC", "-std=c++17", "-shared", "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in inc:
+        cmd += ["-isystem" if d != INCLUDE else "-I", d]
+    lib = os.path.join(root, "lib")
+    cmd += [os.path.join(CSRC, "paged_binding.cpp"), LIB, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-    deps += glob.glob(os.path.join(INCLUDE, "*.h"))
+    deps += glob.glob(os.path.join(INCLUDE, "*.h")) + glob.glob(os.path.join(CSRC, "*.cpp"))
     return any(os.path.getmtime(p) > t for p in deps)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compiles every .cu under csrc/ into one shared library; returns its path."""
+    """Compiles every .cu under csrc/ into one shared library, and the binding; returns the library's path."""
     if not force and not _stale():
         return LIB
     build_dir = os.path.join(PKG, "_build")
@@ -70,9 +94,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if failed:
         raise RuntimeError(f"nvcc failed for {failed}")
     tmp = f"{LIB}.{os.getpid()}.tmp"
-    link = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]
+    link = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-Xlinker", "-soname=libminf.so", "-o", tmp,
+            *objs]
     subprocess.check_call(link)
     os.replace(tmp, LIB)
+    build_binding()
     return LIB
 
 

@@ -681,15 +681,19 @@ __global__ void __launch_bounds__(256, 5) paged_chunk_join_kernel(const __grid_c
 template <class Ty>
 cudaError_t launch_chunk(const ChunkParams &C, cudaStream_t st) {
     const PagedSeqs &S = C.a.seqs;
-    cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<Ty>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmemMax);
+    static std::atomic<unsigned long long> done{0};
+    static std::atomic<int> regs{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(paged_chunk_kernel<Ty>), (int)kSmemMax, done);
     if (e != cudaSuccess) return e;
     // setmaxnreg.inc waits for registers the launch reserved: refuse to launch a
     // build whose register count at entry would make the split wait forever
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, paged_chunk_kernel<Ty>);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (regs.load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, paged_chunk_kernel<Ty>);
+        if (e != cudaSuccess) return e;
+        regs.store(fa.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < kRegsLaunch) return cudaErrorInvalidConfiguration;
     ProfScope prof("paged_chunk", st);
     const int bytes = (int)kSmemPlan + 8 * (S.n_seqs + 1) + 1024;
     paged_chunk_kernel<Ty><<<kGrid, kThreads, bytes, st>>>(C);

@@ -832,8 +832,9 @@ constexpr int kMaxRanges = 64;  // page ranges of a score launch
 template <class Ty, int NT>
 cudaError_t launch_scores(EstimateParams &P, cudaStream_t st) {
     const PagedSeqs &S = P.seqs;
-    cudaError_t e = cudaFuncSetAttribute(paged_scores_kernel<Ty, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)ScoreShape<NT>::kBytes);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(paged_scores_kernel<Ty, NT>), (int)ScoreShape<NT>::kBytes,
+                               done);
     if (e != cudaSuccess) return e;
     // page ranges: about two CTAs to an SM over all (sequence, tile, kv-head)s
     const long long rows = (long long)S.n_seqs * P.tiles * P.hkv;
@@ -860,8 +861,9 @@ cudaError_t launch_select(const EstimateParams &P, cudaStream_t st) {
         return launch_after(paged_select_warp_kernel<Ty, 64>, grid, dim3(kSelectThreads), 0, st, P);
     }
     const size_t bytes = (size_t)P.score_stride * sizeof(uint32_t);
-    cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<Ty>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kMaxBlocks * (int)sizeof(uint32_t));
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(paged_select_kernel<Ty>), kMaxBlocks * (int)sizeof(uint32_t),
+                               done);
     if (e != cudaSuccess) return e;
     return launch_after(paged_select_kernel<Ty>, dim3(rows), dim3(kSelectThreads), bytes, st, P);
 }

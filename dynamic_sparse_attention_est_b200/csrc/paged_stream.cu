@@ -664,8 +664,9 @@ cudaError_t launch_dense(const StreamParams &SP, cudaStream_t st) {
     const PagedAttnParams &P = SP.a;
     const PagedSeqs &S = P.seqs;
     const int bytes = (int)kSmemPre + (S.n_seqs + 1) * (int)sizeof(long long) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(paged_dense_kernel<Ty, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmemPre + (kMaxSeqs + 1) * (int)sizeof(long long) + 1024);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(paged_dense_kernel<Ty, NT>),
+                               (int)kSmemPre + (kMaxSeqs + 1) * (int)sizeof(long long) + 1024, done);
     if (e != cudaSuccess) return e;
     const int rt = (S.max_q * P.group + 8 * NT - 1) / (8 * NT);
     ProfScope prof("paged_dense", st);
@@ -683,8 +684,8 @@ cudaError_t launch_sparse(const StreamParams &SP, cudaStream_t st) {
     const long long items = (long long)P.seqs.total * P.hkv * tiles;
     if (items * P.parts > 0x7fffffffll) return cudaErrorInvalidValue;
     const int bytes = (int)kSmemPre + 1024;
-    cudaError_t e = cudaFuncSetAttribute(paged_sparse_kernel<Ty, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         bytes);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(paged_sparse_kernel<Ty, NT>), bytes, done);
     if (e != cudaSuccess) return e;
     ProfScope prof("paged_sparse", st);
     paged_sparse_kernel<Ty, NT><<<(unsigned)(items * P.parts), kThreads, bytes, st>>>(SP);

@@ -2,7 +2,8 @@
 
 Every function here takes torch CUDA tensors, checks their dtype/layout,
 allocates the outputs and the workspace with torch (PyTorch is the allocator
-and stream provider), and calls the C entry point of the same name.  There is
+and stream provider), and calls the C entry point of the same name (the paged
+calls through the extension module _paged, whose checks cost a microsecond).  There is
 no fallback: if ``libminf.so`` is missing or a call fails, an exception is
 raised.  See ``include/minf.h`` for the semantics of each call.
 """
@@ -375,47 +376,18 @@ def minf_mixed_layer(q, k, v, head_patterns: Sequence[str], last_q: int = 64, n_
 
 
 # ---------------------------------------------------------------- paged cache
-_PAGED_TYPES = {torch.bfloat16: MINF_BF16, torch.float16: MINF_FP16}
+_paged_module = None
 
 
-def _rows(t, name, dev, dtype, total, heads):
-    """A [tokens, heads, 128] tensor as minf_rows: last dimension contiguous, other strides free."""
-    if t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name} must be {dtype} on {dev}")
-    if t.dim() != 3 or t.shape[0] != total or t.shape[1] != heads or t.shape[2] != 128 or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [{total}, {heads}, 128] with a contiguous last dimension")
-    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
+def _paged():
+    """The extension module that hands torch tensors to the paged calls (raises if it was not built)."""
+    global _paged_module
+    if _paged_module is None:
+        lib()
+        from . import _paged as module  # built with libminf.so
 
-
-def _paged_seqs(block_tables, cu_q, kv_lens, max_q_len, total, page_size, num_pages, dev):
-    for name, t, nd in (("block_tables", block_tables, 2), ("cu_q", cu_q, 1), ("kv_lens", kv_lens, 1)):
-        if t.dtype != torch.int32 or t.device != dev or t.dim() != nd or (t.numel() and t.stride(-1) != 1):
-            raise ValueError(f"{name} must be a {nd}-D int32 tensor on {dev} with a contiguous last dimension")
-    n_seqs = kv_lens.shape[0]
-    if cu_q.shape[0] != n_seqs + 1 or block_tables.shape[0] != n_seqs:
-        raise ValueError("cu_q, kv_lens and block_tables disagree on the number of sequences")
-    width = block_tables.shape[1]
-    return PagedSeqs(cu_q.data_ptr(), kv_lens.data_ptr(), block_tables.data_ptr(),
-                     block_tables.stride(0) if n_seqs > 1 else width, width, n_seqs, total,
-                     min(int(max_q_len), total), page_size, num_pages)
-
-
-def _paged_cache(k_cache, v_cache, dev, dtype):
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != dtype or t.device != dev or t.dim() != 4 or t.shape != k_cache.shape or t.shape[3] != 128:
-            raise ValueError(f"{name} must be a {dtype} tensor [pages, hkv, page_size, 128] on {dev}")
-        if t.stride(3) != 1 or t.stride(2) != 128 or (t.shape[1] > 1 and t.stride(1) != t.shape[2] * 128):
-            raise ValueError(f"{name} must be contiguous within a page")
-    num_pages, hkv, page, _ = k_cache.shape
-    least = hkv * page * 128
-    return (PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride(0) if num_pages > 1 else least,
-                       v_cache.stride(0) if num_pages > 1 else least), num_pages, hkv, page)
-
-
-def _paged_type(t, name):
-    if t.dim() != 3 or not t.is_cuda or t.dtype not in _PAGED_TYPES:
-        raise ValueError(f"{name} must be a CUDA bf16 or fp16 tensor [tokens, heads, 128]")
-    return t.device, t.dtype, _PAGED_TYPES[t.dtype]
+        _paged_module = module
+    return _paged_module
 
 
 def paged_workspace_bytes(op: int, hq: int, hkv: int, total: int, n_seqs: int, max_q_len: int, width: int = 0,
@@ -429,104 +401,39 @@ def minf_paged_append(k, v, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q
     """Stores the new tokens' keys (rotated with `rope`, fp32 [positions, rot]) and values in the paged cache,
     updates `k_bounds` [pages, hkv, 2, 128], and returns the rotated queries (q_out, allocated if None; None
     without q).  q, k, v: [tokens, heads, 128], any strides over tokens and heads."""
-    dev, dtype, code = _paged_type(k, "k")
-    total = k.shape[0]
-    cache, num_pages, hkv, page = _paged_cache(k_cache, v_cache, dev, dtype)
-    seqs = _paged_seqs(block_tables, cu_q, kv_lens, max_q_len, total, page, num_pages, dev)
-    rk, rv = _rows(k, "k", dev, dtype, total, hkv), _rows(v, "v", dev, dtype, total, hkv)
-    hq, rq, ro = hkv, None, None
-    if q is not None:
-        hq = q.shape[1]
-        rq = _rows(q, "q", dev, dtype, total, hq)
-        if q_out is None:
-            q_out = torch.empty(total, hq, 128, dtype=dtype, device=dev)
-        ro = _rows(q_out, "q_out", dev, dtype, total, hq)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    rows = rot = 0
-    if rope is not None:
-        if rope.dtype != torch.float32 or rope.device != dev or rope.dim() != 2 or not rope.is_contiguous():
-            raise ValueError(f"rope must be a contiguous fp32 tensor [positions, rot] on {dev}")
-        rows, rot = rope.shape
-    if k_bounds is not None and (k_bounds.dtype != dtype or k_bounds.device != dev or not k_bounds.is_contiguous()
-                                 or tuple(k_bounds.shape) != (num_pages, hkv, 2, 128)):
-        raise ValueError(f"k_bounds must be a contiguous {dtype} tensor [{num_pages}, {hkv}, 2, 128] on {dev}")
-    ws = _ws_for(ws, MINF_STATUS_BYTES, dev)
-    _check(lib().minf_paged_append(ctypes.byref(seqs), code, hq, hkv, 128, ctypes.byref(rk), ctypes.byref(rv),
-                                   rq and ctypes.byref(rq), ro and ctypes.byref(ro), ctypes.byref(cache),
-                                   _ptr(k_bounds), _ptr(rope), rows, rot, int(bool(interleaved)), _ptr(ws),
-                                   ws.numel(), _stream(dev)),
-           "minf_paged_append")
-    return q_out
-
-
-def _paged_out(q, out, want_lse, dev, dtype, total, hq):
-    if out is None:
-        out = torch.empty(total, hq, 128, dtype=dtype, device=dev)
-    lse = torch.empty(total, hq, dtype=torch.float32, device=dev) if want_lse else None
-    return out, _rows(out, "out", dev, dtype, total, hq), lse
+    rc, out, _ = _paged().append(k, v, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q_len, rope, interleaved, q,
+                                 q_out, k_bounds, ws)
+    if rc:
+        _check(rc, "minf_paged_append")
+    return out if q_out is None else q_out
 
 
 def minf_paged_attention(q, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q_len: int,
                          scale: Optional[float] = None, out=None, want_lse: bool = True, ws=None):
     """Causal attention of the new tokens q [tokens, hq, 128] over everything stored; (out, lse [tokens, hq])."""
-    dev, dtype, code = _paged_type(q, "q")
-    total, hq = q.shape[0], q.shape[1]
-    cache, num_pages, hkv, page = _paged_cache(k_cache, v_cache, dev, dtype)
-    seqs = _paged_seqs(block_tables, cu_q, kv_lens, max_q_len, total, page, num_pages, dev)
-    rq = _rows(q, "q", dev, dtype, total, hq)
-    out, ro, lse = _paged_out(q, out, want_lse, dev, dtype, total, hq)
-    if ws is None:
-        ws = workspace(paged_workspace_bytes(OP_PAGED_ATTENTION, hq, hkv, total, seqs.n_seqs, seqs.max_q), dev)
-    _check(lib().minf_paged_attention(ctypes.byref(seqs), code, hq, hkv, 128, ctypes.byref(rq), ctypes.byref(cache),
-                                      _scale(scale), ctypes.byref(ro), _ptr(lse), _ptr(ws), ws.numel(),
-                                      _stream(dev)),
-           "minf_paged_attention")
+    rc, out, lse = _paged().attention(q, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q_len, scale, out, want_lse,
+                                      ws)
+    if rc:
+        _check(rc, "minf_paged_attention")
     return out, lse
 
 
 def minf_paged_block_estimate(q, k_bounds, block_tables, cu_q, kv_lens, max_q_len: int, page_size: int = 64,
                               topk: int = 100, ws=None):
     """Pages selected for every new token and kv-head: (blk_idx [tokens, hkv, topk], blk_cnt [tokens, hkv])."""
-    dev, dtype, code = _paged_type(q, "q")
-    total, hq = q.shape[0], q.shape[1]
-    if k_bounds.dtype != dtype or k_bounds.device != dev or k_bounds.dim() != 4 or not k_bounds.is_contiguous() \
-            or tuple(k_bounds.shape[2:]) != (2, 128):
-        raise ValueError(f"k_bounds must be a contiguous {dtype} tensor [pages, hkv, 2, 128] on {dev}")
-    num_pages, hkv = k_bounds.shape[0], k_bounds.shape[1]
-    seqs = _paged_seqs(block_tables, cu_q, kv_lens, max_q_len, total, page_size, num_pages, dev)
-    rq = _rows(q, "q", dev, dtype, total, hq)
-    idx = torch.empty(total, hkv, topk, dtype=torch.int32, device=dev)
-    cnt = torch.empty(total, hkv, dtype=torch.int32, device=dev)
-    if ws is None:
-        ws = workspace(paged_workspace_bytes(OP_PAGED_BLOCK_ESTIMATE, hq, hkv, total, seqs.n_seqs, seqs.max_q,
-                                             seqs.width, topk), dev)
-    _check(lib().minf_paged_block_estimate(ctypes.byref(seqs), code, hq, hkv, 128, ctypes.byref(rq), _ptr(k_bounds),
-                                           topk, _ptr(idx), _ptr(cnt), _ptr(ws), ws.numel(), _stream(dev)),
-           "minf_paged_block_estimate")
+    rc, idx, cnt = _paged().block_estimate(q, k_bounds, block_tables, cu_q, kv_lens, max_q_len, page_size, topk, ws)
+    if rc:
+        _check(rc, "minf_paged_block_estimate")
     return idx, cnt
 
 
 def minf_paged_block_attention(q, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q_len: int, blk_idx, blk_cnt,
                                scale: Optional[float] = None, out=None, want_lse: bool = True, ws=None):
     """Causal attention of every new token over its listed pages only; (out, lse [tokens, hq])."""
-    dev, dtype, code = _paged_type(q, "q")
-    total, hq = q.shape[0], q.shape[1]
-    cache, num_pages, hkv, page = _paged_cache(k_cache, v_cache, dev, dtype)
-    seqs = _paged_seqs(block_tables, cu_q, kv_lens, max_q_len, total, page, num_pages, dev)
-    rq = _rows(q, "q", dev, dtype, total, hq)
-    for name, t, shape in (("blk_idx", blk_idx, (total, hkv, blk_idx.shape[-1])), ("blk_cnt", blk_cnt, (total, hkv))):
-        if t.dtype != torch.int32 or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {dev}")
-    topk = blk_idx.shape[2]
-    out, ro, lse = _paged_out(q, out, want_lse, dev, dtype, total, hq)
-    if ws is None:
-        ws = workspace(paged_workspace_bytes(OP_PAGED_BLOCK_ATTENTION, hq, hkv, total, seqs.n_seqs, seqs.max_q,
-                                             seqs.width, topk), dev)
-    _check(lib().minf_paged_block_attention(ctypes.byref(seqs), code, hq, hkv, 128, ctypes.byref(rq),
-                                            ctypes.byref(cache), _scale(scale), _ptr(blk_idx), _ptr(blk_cnt), topk,
-                                            ctypes.byref(ro), _ptr(lse), _ptr(ws), ws.numel(), _stream(dev)),
-           "minf_paged_block_attention")
+    rc, out, lse = _paged().block_attention(q, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q_len, blk_idx, blk_cnt,
+                                            scale, out, want_lse, ws)
+    if rc:
+        _check(rc, "minf_paged_block_attention")
     return out, lse
 
 
