@@ -219,30 +219,29 @@ struct PagedAttnParams {
     const int *blk_idx, *blk_cnt;       // per-token page lists (null: every stored page)
     int topk;
     // partial states of split work: unnormalised O [slot][rows][128], (max, sum)
-    // [slot][rows] and, per slot, the work item it belongs to (-1: unused)
+    // [slot][rows]; and the kernel's plan, for the one that joins them
     float *part_o;
     float2 *part_ml;
-    int *part_item;
-    int n_slots, parts;
+    long long *plan;
+    int n_slots;
     WsHeader *hdr;
     unsigned long long wait_limit_ns;
 };
-// Sizes of the streaming kernel's split: query rows per tile, parts per item
-// (page lists), partial slots, and entries of the item table (dense).
+// The streaming kernel's query rows per tile, and partial slots: two to a CTA that
+// takes a share of the work (page lists: 0 with a CTA to each item).
 struct StreamPlan {
-    int rows, parts, n_slots;
-    long long n_items;
+    int rows, n_slots;
 };
-StreamPlan paged_stream_plan(int n_seqs, int hkv, int group, int max_q);
+StreamPlan paged_stream_plan(int group, int max_q);
 StreamPlan paged_sparse_plan(int total, int hkv, int group, int topk, int page);
 cudaError_t run_paged_stream(const PagedAttnParams &P, bool fp16, int rows, cudaStream_t st);
 cudaError_t run_paged_sparse(const PagedAttnParams &P, bool fp16, int rows, cudaStream_t st);
 
-// The chunk kernel's partial slots, their rows, and entries of its plan table.
+// The chunk kernel's partial slots, and their rows.
 struct ChunkPlan {
-    int part_rows, n_slots, n_items;
+    int part_rows, n_slots;
 };
-ChunkPlan paged_chunk_plan(int n_seqs, int group, int max_q);
+ChunkPlan paged_chunk_plan(int group, int max_q);
 cudaError_t run_paged_chunk(const PagedAttnParams &P, bool fp16, int part_rows, cudaStream_t st);
 
 constexpr int kMaxBlocks = 32768;  // pages of a sequence the selection handles

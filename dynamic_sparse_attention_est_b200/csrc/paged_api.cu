@@ -114,28 +114,28 @@ constexpr int kStreamMaxRows = 16;
 bool streams(int max_q, int group) { return (long long)max_q * group <= kStreamMaxRows; }
 
 struct AttnSizes {
-    size_t o, ml, item, total;
+    size_t o, ml, plan, total;
 };
-AttnSizes attn_sizes(long long n_slots, int rows, long long n_item) {
+AttnSizes attn_sizes(long long n_slots, int rows, long long n_plan) {
     AttnSizes z{};
     size_t off = MINF_STATUS_BYTES;
     z.o = off;
     off = round_up(off + (size_t)n_slots * rows * kD * sizeof(float));
     z.ml = off;
     off = round_up(off + (size_t)n_slots * rows * sizeof(float2));
-    z.item = off;
-    off = round_up(off + (size_t)n_item * sizeof(int));
+    z.plan = off;
+    off = round_up(off + (size_t)n_plan * sizeof(long long));
     z.total = off;
     return z;
 }
 
-AttnSizes dense_sizes(int n_seqs, int hkv, int group, int max_q) {
+AttnSizes dense_sizes(int n_seqs, int group, int max_q) {
     if (streams(max_q, group)) {
-        const StreamPlan p = paged_stream_plan(n_seqs, hkv, group, max_q);
-        return attn_sizes(p.n_slots, p.rows, p.n_slots + p.n_items);
+        const StreamPlan p = paged_stream_plan(group, max_q);
+        return attn_sizes(p.n_slots, p.rows, n_seqs + 1);
     }
-    const ChunkPlan p = paged_chunk_plan(n_seqs, group, max_q);
-    return attn_sizes(p.n_slots, p.part_rows, p.n_items);
+    const ChunkPlan p = paged_chunk_plan(group, max_q);
+    return attn_sizes(p.n_slots, p.part_rows, n_seqs + 2);
 }
 
 AttnSizes sparse_sizes(int total, int hkv, int group, int topk, int page) {
@@ -153,7 +153,7 @@ void place(PagedAttnParams &P, const AttnSizes &z, void *ws) {
     char *b = static_cast<char *>(ws);
     P.part_o = reinterpret_cast<float *>(b + z.o);
     P.part_ml = reinterpret_cast<float2 *>(b + z.ml);
-    P.part_item = reinterpret_cast<int *>(b + z.item);
+    P.plan = reinterpret_cast<long long *>(b + z.plan);
     P.hdr = static_cast<WsHeader *>(ws);
     P.wait_limit_ns = api_wait_limit_ns();
 }
@@ -184,7 +184,6 @@ int fill_attn(PagedAttnParams &P, const minf_paged_seqs *seqs, int dtype, int hq
     P.hkv = hkv;
     P.group = hq / hkv;
     P.scale_log2 = scale * 1.4426950408889634f;
-    P.parts = 1;
     return MINF_OK;
 }
 
@@ -224,13 +223,13 @@ size_t minf_paged_workspace_bytes(int op, int hq, int hkv, int total, int n_seqs
     case MINF_OP_PAGED_APPEND:
         return MINF_STATUS_BYTES;
     case MINF_OP_PAGED_ATTENTION:
-        return dense_sizes(n_seqs, hkv, hq / hkv, max_q).total;
+        return dense_sizes(n_seqs, hq / hkv, max_q).total;
     case MINF_OP_PAGED_BLOCK_ESTIMATE:
         if (topk < 1 || width < 1 || width > kMaxBlocks) return 0;
         return estimate_bytes(paged_estimate_plan(total, n_seqs, max_q, hkv, width), nullptr);
     case MINF_OP_PAGED_BLOCK_ATTENTION:
         if (topk < 1) return 0;
-        return sparse_sizes(total, hkv, hq / hkv, topk, 128).total;  // the largest pages make the most parts
+        return sparse_sizes(total, hkv, hq / hkv, topk, 128).total;  // the largest pages make the most shares
     }
     return 0;
 }
@@ -298,19 +297,19 @@ int minf_paged_attention(const minf_paged_seqs *seqs, int dtype, int hq, int hkv
     if (rc) return rc;
     const PagedSeqs &S = P.seqs;
     const bool none = S.n_seqs == 0 || S.total == 0;
-    const AttnSizes z = none ? AttnSizes{0, 0, 0, MINF_STATUS_BYTES} : dense_sizes(S.n_seqs, hkv, P.group, S.max_q);
+    const AttnSizes z = none ? AttnSizes{0, 0, 0, MINF_STATUS_BYTES} : dense_sizes(S.n_seqs, P.group, S.max_q);
     if ((rc = api_check_ws(ws, ws_bytes, z.total))) return rc;
     if (none) return MINF_OK;
     place(P, z, ws);
     const DeviceScope scope;
     if ((rc = api_select_device(cache->k))) return rc;
     if (streams(S.max_q, P.group)) {
-        const StreamPlan p = paged_stream_plan(S.n_seqs, hkv, P.group, S.max_q);
+        const StreamPlan p = paged_stream_plan(P.group, S.max_q);
         P.n_slots = p.n_slots;
         return launch_result(run_paged_stream(P, dtype == MINF_FP16, p.rows, (cudaStream_t)stream),
                              "paged attention launch");
     }
-    const ChunkPlan p = paged_chunk_plan(S.n_seqs, P.group, S.max_q);
+    const ChunkPlan p = paged_chunk_plan(P.group, S.max_q);
     P.n_slots = p.n_slots;
     return launch_result(run_paged_chunk(P, dtype == MINF_FP16, p.part_rows, (cudaStream_t)stream),
                          "paged attention launch");
@@ -373,7 +372,6 @@ int minf_paged_block_attention(const minf_paged_seqs *seqs, int dtype, int hq, i
     P.blk_idx = blk_idx;
     P.blk_cnt = blk_cnt;
     P.topk = topk;
-    P.parts = p.parts;
     P.n_slots = p.n_slots;
     const DeviceScope scope;
     if ((rc = api_select_device(cache->k))) return rc;

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     tc_fence_after();
     const int n_units = pre[S.n_seqs].x;
     if (blockIdx.x == 0 && warp == 3) {  // the joining kernel's copy: (slots, pairs) cut before each sequence
-        int2 *dst = reinterpret_cast<int2 *>(P.a.part_item + 2);
+        int2 *dst = reinterpret_cast<int2 *>(P.a.plan + 1);
         int cut = 0;
         for (int s0 = 0; s0 <= S.n_seqs; s0 += 32) {
             const int s = s0 + lane;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             if (s <= S.n_seqs) dst[s] = make_int2(pre[s].y, cut + inc - mine);
             cut += __shfl_sync(0xffffffffu, inc, 31);
         }
-        if (lane == 0) P.a.part_item[0] = part_len;
+        if (lane == 0) P.a.plan[0] = part_len;
     }
     const uint32_t tmem = *tmem_slot;
     const WaitCtl wc{abort_flag, &P.a.hdr->status, P.a.wait_limit_ns};
@@ -628,8 +628,8 @@ __global__ void __launch_bounds__(256, 5) paged_chunk_join_kernel(const __grid_c
     const PagedSeqs &S = P.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     wait_for_primary();
-    const int part_len = P.part_item[0];
-    const int2 *pre = reinterpret_cast<const int2 *>(P.part_item + 2);  // (slots, pairs) cut before each sequence
+    const int part_len = (int)P.plan[0];
+    const int2 *pre = reinterpret_cast<const int2 *>(P.plan + 1);  // (slots, pairs) cut before each sequence
     const int n_pairs = pre[S.n_seqs].y;
     const int per = part_rows / kJoinRows;
     for (int w = blockIdx.x; w < n_pairs * per; w += gridDim.x) {
@@ -704,13 +704,7 @@ cudaError_t launch_chunk(const ChunkParams &C, cudaStream_t st) {
 
 }  // namespace
 
-ChunkPlan paged_chunk_plan(int n_seqs, int group, int max_q) {
-    ChunkPlan p{};
-    p.part_rows = max_q <= 128 / group ? 128 : 256;
-    p.n_slots = 8 * kGrid;
-    p.n_items = 2 + 2 * (n_seqs + 1);
-    return p;
-}
+ChunkPlan paged_chunk_plan(int group, int max_q) { return {max_q <= 128 / group ? 128 : 256, 8 * kGrid}; }
 
 cudaError_t run_paged_chunk(const PagedAttnParams &P, bool fp16, int part_rows, cudaStream_t st) {
     const PagedSeqs &S = P.seqs;

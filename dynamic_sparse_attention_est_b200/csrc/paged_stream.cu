@@ -18,10 +18,12 @@
 //     32 rows for each one used.
 //   * Running maximum and sum per row in fp32, log2 domain; the maximum moves
 //     only past a margin, which one vote per group decides.
-//   * Dense items are cut at equal shares of all 16-key groups of the call (each
-//     CTA takes the prefix sums of the lengths itself, so that a captured launch
-//     follows them), however uneven the lengths; an item's parts are joined by a
-//     second small kernel in a fixed order.
+//   * The work of a call is cut into equal shares, one for each CTA of a single wave,
+//     wherever in an item a share ends: the 16-key groups of all sequences (each CTA
+//     takes the prefix sums of the lengths itself, so that a captured launch follows
+//     them), or the entries of all page lists.  An item's parts are joined by a second
+//     small kernel in a fixed order.
+#include <algorithm>
 #include <cstring>
 
 #include "internal.h"
@@ -390,7 +392,8 @@ __device__ __forceinline__ void run_piece(const StreamParams &SP, const Item &it
 }
 
 // Barriers and ring of the calling warp; the whole CTA calls it.
-__device__ __forceinline__ Ring ring_init(uint8_t *smem, WaitCtl &wc, const PagedAttnParams &P) {
+__device__ __forceinline__ Ring ring_init(uint8_t *smem, WaitCtl &wc, const StreamParams &SP) {
+    const PagedAttnParams &P = SP.a;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kSmemBar);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + kWarps * kStages);
     const int warp = threadIdx.x >> 5;
@@ -398,6 +401,9 @@ __device__ __forceinline__ Ring ring_init(uint8_t *smem, WaitCtl &wc, const Page
         for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(bars + i), 1);
         *abort_flag = 0;
         fence_mbar_init();
+    } else if (threadIdx.x == 32) {
+        tma_prefetch_desc(&SP.tmap_k);
+        tma_prefetch_desc(&SP.tmap_v);
     }
     __syncthreads();
     wc.abort_flag = abort_flag;
@@ -411,6 +417,12 @@ __device__ __forceinline__ uint8_t *align_1k(uint8_t *p) {
 }
 
 static_assert(kWarps * 16 * (kOPad * 4 + 8) <= kRingBytes, "the join buffer fits over the rings");
+
+// CTAs that share `total` 16-key groups: a group to each warp at least, so that none
+// of them is without work and an item's parts sit in consecutive CTAs.
+__device__ __forceinline__ int dense_ctas(long long total) {
+    return (int)min((long long)kStreamGrid, max(1ll, total / kWarps));
+}
 
 // ------------------------------------------------------------------ dense
 // Work units: 16-key groups, sequence after sequence; within one, (kv-head, row
@@ -426,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dense_kernel(const __grid_c
     const PagedAttnParams &P = SP.a;
     const PagedSeqs &S = P.seqs;
     WaitCtl wc;
-    Ring ring = ring_init(smem, wc, P);
+    Ring ring = ring_init(smem, wc, SP);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const int per = (S.n_seqs + kThreads - 1) / kThreads;
@@ -459,7 +471,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dense_kernel(const __grid_c
     }
     __syncthreads();
     const long long total = pre[S.n_seqs];
-    const int rt_max = (S.max_q * P.group + 8 * NT - 1) / (8 * NT);
+    if (blockIdx.x == 0)  // the joining kernel's copy
+        for (int x = threadIdx.x; x <= S.n_seqs; x += kThreads) P.plan[x] = pre[x];
+    launch_dependents();
 
     // sequences with new tokens and nothing stored: their rows see no key
     for (int s = blockIdx.x; s < S.n_seqs; s += gridDim.x) {
@@ -471,17 +485,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dense_kernel(const __grid_c
                                       (long long)hh * P.o_hs)[i & 15] = make_uint4(0, 0, 0, 0);
             if ((i & 15) == 0 && P.lse) P.lse[(size_t)tok * P.hq + hh] = -INFINITY;
         }
-        for (int i = threadIdx.x; i < P.hkv * rt_max; i += kThreads)
-            P.part_item[P.n_slots + s * P.hkv * rt_max + i] = -1;
     }
 
-    // CTAs that share the units: one 16-key group to a warp at least, so that none of
-    // them is without work (an item's parts then sit in consecutive CTAs)
-    const long long n_cta = min((long long)gridDim.x, max(1ll, total / kWarps));
-    const long long me = min((long long)blockIdx.x, n_cta);
-    const long long u0 = total * me / n_cta, u1 = total * min(me + 1, n_cta) / n_cta;
-    int slot_item[2] = {-1, -1};
-    int n_piece = 0;
+    const int n_cta = dense_ctas(total);
+    const long long me = min((int)blockIdx.x, n_cta);
+    const long long u0 = total * me / n_cta, u1 = total * min(me + 1, (long long)n_cta) / n_cta;
     long long u = u0;
     int s = 0;
     {
@@ -509,23 +517,18 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dense_kernel(const __grid_c
         it.tok0 = v.q0;
         it.pos0 = v.len - v.n;
         it.len = v.len;
-        const int id = (s * P.hkv + it.h) * rt_max + in_seq % tiles;
         const bool whole = ga == 0 && gb == groups;
-        const int which = n_piece == 0 ? 0 : 1;  // a cut piece is a CTA's first or its last
-        const int slot = whole ? -1 : 2 * (int)blockIdx.x + which;
-        if (!whole) slot_item[which] = id;
-        // the item's first slot, for the joining kernel (-1: already whole)
-        if (ga == 0 && threadIdx.x == 0) P.part_item[P.n_slots + id] = slot;
+        // a cut piece is a CTA's first or its last
+        const int slot = whole ? -1 : 2 * (int)blockIdx.x + (u == u0 ? 0 : 1);
         run_piece<Ty, NT, false>(SP, it, nullptr, 0, ga, gb, slot, ring, wc, sm_o, sm_ml);
         u += gb - ga;
-        ++n_piece;
     }
-    if (threadIdx.x < 2) P.part_item[2 * blockIdx.x + threadIdx.x] = threadIdx.x ? slot_item[1] : slot_item[0];
-    launch_dependents();
 }
 
 // ------------------------------------------------------------------ selected pages
-// One CTA per (token, kv-head, row tile) and part of its page list.
+// Work units: entries of the page lists (topk to an item, those behind its count
+// empty), item after item; an item is a (token, kv-head, row tile).  CTA c of C takes
+// units [U c / C, U (c + 1) / C); with a CTA to each item, that is its list.
 template <class Ty, int NT>
 __global__ void __launch_bounds__(kThreads, 2) paged_sparse_kernel(const __grid_constant__ StreamParams SP) {
     extern __shared__ uint8_t smem_raw[];
@@ -536,43 +539,52 @@ __global__ void __launch_bounds__(kThreads, 2) paged_sparse_kernel(const __grid_
     const PagedAttnParams &P = SP.a;
     const PagedSeqs &S = P.seqs;
     WaitCtl wc;
-    Ring ring = ring_init(smem, wc, P);
-    const int part = blockIdx.x % P.parts, item = blockIdx.x / P.parts;
-    const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
-    const int rt = item % tiles, h = (item / tiles) % P.hkv, t = item / tiles / P.hkv;
-    if (threadIdx.x == 0) found = -1;
-    __syncthreads();
-    for (int s = threadIdx.x; s < S.n_seqs; s += kThreads)
-        if (__ldg(S.cu_q + s) <= t && t < __ldg(S.cu_q + s + 1)) found = s;
-    __syncthreads();
-    const int s = found;
-    if (s < 0) return;  // a row behind the last sequence
-    const SeqView v = seq_view(S, s, P.hdr);
-    if (v.n == 0) return;
-    Item it;
-    it.seq = s;
-    it.h = h;
-    it.row0 = rt * 8 * NT;
-    it.rows = min(8 * NT, P.group - it.row0);
-    it.tok0 = t;
-    it.pos0 = v.len - v.n + (t - v.q0);
-    it.len = v.len;
-    const int li = t * P.hkv + h;
-    int cnt = __ldg(P.blk_cnt + li);
-    if (cnt < 0 || cnt > P.topk) {
-        flag_invalid(P.hdr, BAD_BLOCK);
-        cnt = max(0, min(cnt, P.topk));
-    }
-    if (it.pos0 < 0) cnt = 0;
-    const int gp = S.page >> 4;
-    const int a = (int)((long long)cnt * part / P.parts), b = (int)((long long)cnt * (part + 1) / P.parts);
-    run_piece<Ty, NT, true>(SP, it, P.blk_idx + (long long)li * P.topk, cnt, a * gp, b * gp,
-                            P.parts > 1 ? item * P.parts + part : -1, ring, wc, sm_o, sm_ml);
+    Ring ring = ring_init(smem, wc, SP);
     launch_dependents();
+    const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
+    const long long total = (long long)S.total * P.hkv * tiles * P.topk;
+    const long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+    const int gp = S.page >> 4;
+    for (long long u = u0; u < u1;) {
+        const int item = (int)(u / P.topk), a = (int)(u % P.topk);
+        const int b = (int)min((long long)P.topk, a + (u1 - u));
+        const int slot = a == 0 && b == P.topk ? -1 : 2 * (int)blockIdx.x + (u == u0 ? 0 : 1);
+        u += b - a;
+        const int rt = item % tiles, h = (item / tiles) % P.hkv, t = item / tiles / P.hkv;
+        if (threadIdx.x == 0) found = -1;
+        __syncthreads();
+        for (int s = threadIdx.x; s < S.n_seqs; s += kThreads)
+            if (__ldg(S.cu_q + s) <= t && t < __ldg(S.cu_q + s + 1)) found = s;
+        __syncthreads();
+        const int s = found;
+        __syncthreads();        // read by all before it is set again
+        if (s < 0) continue;  // a row behind the last sequence
+        const SeqView v = seq_view(S, s, P.hdr);
+        if (v.n == 0) continue;
+        Item it;
+        it.seq = s;
+        it.h = h;
+        it.row0 = rt * 8 * NT;
+        it.rows = min(8 * NT, P.group - it.row0);
+        it.tok0 = t;
+        it.pos0 = v.len - v.n + (t - v.q0);
+        it.len = v.len;
+        const int li = t * P.hkv + h;
+        int cnt = __ldg(P.blk_cnt + li);
+        if (cnt < 0 || cnt > P.topk) {
+            flag_invalid(P.hdr, BAD_BLOCK);
+            cnt = max(0, min(cnt, P.topk));
+        }
+        if (it.pos0 < 0) cnt = 0;
+        run_piece<Ty, NT, true>(SP, it, P.blk_idx + (long long)li * P.topk, cnt, min(a, cnt) * gp, min(b, cnt) * gp, slot,
+                                ring, wc, sm_o, sm_ml);
+    }
 }
 
 // ------------------------------------------------------------------ join
-// One CTA per (item, row): the parts in order, a quarter of them to each warp.
+// One CTA per (item, row): the parts in order, a quarter of them to each warp.  Which
+// parts an item has follows from its units and the shares, as the kernel before cut
+// them.
 template <class Ty, int NT, bool kSparse>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams P) {
     __shared__ float4 so[kWarps][32];
@@ -580,8 +592,8 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     const PagedSeqs &S = P.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int id = blockIdx.x, row = blockIdx.y;
-    wait_for_primary();
-    int h, x, tok0, first, n_part;
+    int h, x, tok0, n_cta;
+    long long first, units, total;  // the item's units, of all
     if (kSparse) {
         const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
         h = (id / tiles) % P.hkv;
@@ -593,32 +605,31 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
         for (int s = threadIdx.x; s < S.n_seqs; s += kThreads)
             if (__ldg(S.cu_q + s) <= tok0 && tok0 < __ldg(S.cu_q + s + 1) && seq_view(S, s, P.hdr).n > 0) hit = s;
         if (!__syncthreads_or(hit >= 0)) return;
-        first = id * P.parts;
-        n_part = P.parts;
+        units = P.topk;
+        first = (long long)id * units;
+        total = (long long)S.total * P.hkv * tiles * units;
+        n_cta = P.n_slots / 2;
+        wait_for_primary();
     } else {
         const int rt_max = (S.max_q * P.group + 8 * NT - 1) / (8 * NT);
-        const int s = id / rt_max / P.hkv;
+        const int s = id / rt_max / P.hkv, rt = id % rt_max;
         h = (id / rt_max) % P.hkv;
-        x = (id % rt_max) * 8 * NT + row;
+        x = rt * 8 * NT + row;
         const SeqView v = seq_view(S, s, P.hdr);
         tok0 = v.q0;
-        if (x >= v.n * P.group) return;
-        first = P.part_item[P.n_slots + id];
-        if (first < 0) return;
-        n_part = 1;
-        for (int i0 = 1;; i0 += 32) {  // the parts that follow sit in every second slot
-            const int sl_i = 2 * (first / 2 + i0 + lane);
-            const bool same = sl_i < P.n_slots && P.part_item[sl_i] == id;
-            const unsigned bal = __ballot_sync(0xffffffffu, same);
-            const int run = bal == 0xffffffffu ? 32 : __ffs(~bal) - 1;
-            n_part += run;
-            if (run < 32) break;
-        }
+        if (x >= v.n * P.group || v.len == 0) return;
+        units = (v.len + kGroup - 1) / kGroup;
+        wait_for_primary();
+        total = P.plan[S.n_seqs];
+        first = P.plan[s] + (h * (long long)((v.n * P.group + 8 * NT - 1) / (8 * NT)) + rt) * units;
+        n_cta = dense_ctas(total);
     }
-    auto slot_of = [&](int i) -> size_t {
-        const int sidx = kSparse ? first + i : (i == 0 ? first : 2 * (first / 2 + i));
-        return (size_t)sidx * 8 * NT + row;
-    };
+    // CTA c holds units total c / n_cta .. total (c + 1) / n_cta - 1
+    const int c0 = (int)(((first + 1) * n_cta - 1) / total), c1 = (int)(((first + units) * n_cta - 1) / total);
+    if (c0 == c1) return;  // whole, already written
+    const int n_part = c1 - c0 + 1;
+    const int slot0 = 2 * c0 + (first == total * c0 / n_cta ? 0 : 1);
+    auto slot_of = [&](int i) -> size_t { return (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * 8 * NT + row; };
     float m = -INFINITY;
     for (int i = lane; i < n_part; i += 32) m = fmaxf(m, P.part_ml[slot_of(i)].x);
 #pragma unroll
@@ -680,17 +691,17 @@ cudaError_t launch_dense(const StreamParams &SP, cudaStream_t st) {
 template <class Ty, int NT>
 cudaError_t launch_sparse(const StreamParams &SP, cudaStream_t st) {
     const PagedAttnParams &P = SP.a;
-    const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
-    const long long items = (long long)P.seqs.total * P.hkv * tiles;
-    if (items * P.parts > 0x7fffffffll) return cudaErrorInvalidValue;
+    const long long items = (long long)P.seqs.total * P.hkv * ((P.group + 8 * NT - 1) / (8 * NT));
+    if (items > 0x7fffffffll) return cudaErrorInvalidValue;
+    const unsigned ctas = P.n_slots > 0 ? P.n_slots / 2 : (unsigned)items;
     const int bytes = (int)kSmemPre + 1024;
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(paged_sparse_kernel<Ty, NT>), bytes, done);
     if (e != cudaSuccess) return e;
     ProfScope prof("paged_sparse", st);
-    paged_sparse_kernel<Ty, NT><<<(unsigned)(items * P.parts), kThreads, bytes, st>>>(SP);
+    paged_sparse_kernel<Ty, NT><<<ctas, kThreads, bytes, st>>>(SP);
     e = cudaGetLastError();
-    if (e != cudaSuccess || P.parts == 1) return e;
+    if (e != cudaSuccess || P.n_slots == 0) return e;
     return launch_after(paged_join_kernel<Ty, NT, true>, dim3((unsigned)items, min(8 * NT, P.group)), dim3(kThreads), 0,
                         st, P);
 }
@@ -706,26 +717,17 @@ cudaError_t stream_maps(StreamParams &SP, const PagedAttnParams &P, bool fp16) {
 
 }  // namespace
 
-StreamPlan paged_stream_plan(int n_seqs, int hkv, int group, int max_q) {
-    StreamPlan p{};
-    p.rows = max_q * group <= 8 ? 8 : 16;
-    p.parts = 1;
-    p.n_slots = 2 * kStreamGrid;
-    p.n_items = (long long)n_seqs * hkv * ((max_q * group + p.rows - 1) / p.rows);
-    return p;
-}
+StreamPlan paged_stream_plan(int group, int max_q) { return {max_q * group <= 8 ? 8 : 16, 2 * kStreamGrid}; }
 
 StreamPlan paged_sparse_plan(int total, int hkv, int group, int topk, int page) {
-    StreamPlan p{};
-    p.rows = group <= 8 ? 8 : 16;
-    const long long items = (long long)total * hkv * ((group + p.rows - 1) / p.rows);
-    // parts until the machine is filled, at least one 16-key group to a warp
-    long long parts = items > 0 ? (kStreamGrid + items - 1) / items : 1;
-    parts = min(parts, max(1ll, (long long)topk * page / (kGroup * kWarps)));
-    p.parts = (int)min(parts, (long long)topk);
-    p.n_slots = p.parts > 1 ? (int)(items * p.parts) : 0;
-    p.n_items = 0;
-    return p;
+    const int rows = group <= 8 ? 8 : 16;
+    const long long items = (long long)total * hkv * ((group + rows - 1) / rows);
+    // From four waves of items on, a CTA to each (their pages meet in L2 while neighbouring
+    // tokens run side by side); below, equal shares of one wave, of a 16-key group to a
+    // warp at least.
+    if (items >= 4 * kStreamGrid) return {rows, 0};
+    const long long shares = std::min<long long>({kStreamGrid, items * topk, items * topk * page / (kGroup * kWarps)});
+    return {rows, 2 * (int)std::max(1ll, shares)};
 }
 
 cudaError_t run_paged_stream(const PagedAttnParams &P, bool fp16, int rows, cudaStream_t st) {
