@@ -8,8 +8,8 @@
 // share their pages.  The kernel is built around the loads.
 //
 //   * Warps take 16-key groups and keep a softmax state of their own; nothing
-//     synchronises until the end of an item.  Each warp feeds itself: a ring of
-//     kStages groups (8 KB of K and V each) that its first lane fills by TMA, 192 KB
+//     synchronises until the end of an item.  Each warp feeds itself: a ring of two
+//     or three groups (8 KB of K and V each) that its first lane fills by TMA, 192 KB
 //     in flight on an SM.  The boxes are 128-byte swizzled, so ldmatrix reads them
 //     without bank conflicts.
 //   * With keys on the 16-row side and query rows on the 8-column side
@@ -33,17 +33,23 @@ namespace minf {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
 constexpr int kGroup = 16;         // keys per warp step
-constexpr int kStages = 3;         // groups in flight per warp
 constexpr int kStreamGrid = 296;   // two CTAs (their rings: 192 KB) on each of 148 SMs
 constexpr int kOPad = 132;         // floats per row of the CTA's join buffer
 constexpr uint32_t kBoxBytes = 2048;             // 16 keys x 64 channels
 constexpr uint32_t kStageBytes = 4 * kBoxBytes;  // K low, K high, V low, V high channels
-constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
+constexpr uint32_t kRingBytes = 12 * kStageBytes;
 constexpr uint32_t kSmemBar = kRingBytes;         // mbarriers, abort flag
 constexpr uint32_t kSmemPre = kSmemBar + 256;     // [n_seqs + 1] units before a sequence (dense)
+
+// Warps of a CTA and groups in flight to each, by the registers that NT row tiles
+// take: six warps of two with one tile (313 tokens with 64 pages of 32: 64.6 us; four of
+// three: 75.4 us), four of three with two tiles.
+template <int NT>
+struct Shape {
+    static constexpr int kWarps = NT == 1 ? 6 : 4, kStages = 12 / kWarps, kThreads = 32 * kWarps;
+};
+constexpr int kJoinWarps = 4;
 
 struct StreamParams {
     CUtensorMap tmap_k;  // {128, P, hkv, pages}, box {64, 16, 1, 1}
@@ -233,6 +239,7 @@ __device__ __forceinline__ void run_piece(const StreamParams &SP, const Item &it
                                           int g1, int slot, Ring &ring, const WaitCtl &wc, float *sm_o,
                                           float2 *sm_ml) {
     using T = typename Ty::T;
+    constexpr int kWarps = Shape<NT>::kWarps, kStages = Shape<NT>::kStages;
     const PagedAttnParams &P = SP.a;
     const PagedSeqs &S = P.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -392,7 +399,9 @@ __device__ __forceinline__ void run_piece(const StreamParams &SP, const Item &it
 }
 
 // Barriers and ring of the calling warp; the whole CTA calls it.
+template <int NT>
 __device__ __forceinline__ Ring ring_init(uint8_t *smem, WaitCtl &wc, const StreamParams &SP) {
+    constexpr int kWarps = Shape<NT>::kWarps, kStages = Shape<NT>::kStages;
     const PagedAttnParams &P = SP.a;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kSmemBar);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + kWarps * kStages);
@@ -416,19 +425,26 @@ __device__ __forceinline__ uint8_t *align_1k(uint8_t *p) {
     return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-static_assert(kWarps * 16 * (kOPad * 4 + 8) <= kRingBytes, "the join buffer fits over the rings");
+static_assert(6 * 8 * (kOPad * 4 + 8) <= kRingBytes && 4 * 16 * (kOPad * 4 + 8) <= kRingBytes, "the join buffer fits over the rings");
 
-// CTAs that share `total` 16-key groups: a group to each warp at least, so that none
+// CTAs that share `total` 16-key groups: four groups at least to each, so that none
 // of them is without work and an item's parts sit in consecutive CTAs.
 __device__ __forceinline__ int dense_ctas(long long total) {
-    return (int)min((long long)kStreamGrid, max(1ll, total / kWarps));
+    return (int)min((long long)kStreamGrid, max(1ll, total >> 2));
+}
+// a / b for a >= 0, b > 0: the 64-bit division takes a fifth of a microsecond, and
+// nearly all calls fit 32 bits.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+    return ((unsigned long long)(a | b) >> 32) ? a / b : (long long)((unsigned)a / (unsigned)b);
 }
 
 // ------------------------------------------------------------------ dense
 // Work units: 16-key groups, sequence after sequence; within one, (kv-head, row
 // tile) after one another.  CTA c of C takes units [U c / C, U (c + 1) / C).
 template <class Ty, int NT>
-__global__ void __launch_bounds__(kThreads, 2) paged_dense_kernel(const __grid_constant__ StreamParams SP) {
+__global__ void __launch_bounds__(Shape<NT>::kThreads, 2)
+    paged_dense_kernel(const __grid_constant__ StreamParams SP) {
+    constexpr int kWarps = Shape<NT>::kWarps, kThreads = Shape<NT>::kThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_1k(smem_raw);
     float *sm_o = reinterpret_cast<float *>(smem);
@@ -438,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dense_kernel(const __grid_c
     const PagedAttnParams &P = SP.a;
     const PagedSeqs &S = P.seqs;
     WaitCtl wc;
-    Ring ring = ring_init(smem, wc, SP);
+    Ring ring = ring_init<NT>(smem, wc, SP);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const int per = (S.n_seqs + kThreads - 1) / kThreads;
@@ -489,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dense_kernel(const __grid_c
 
     const int n_cta = dense_ctas(total);
     const long long me = min((int)blockIdx.x, n_cta);
-    const long long u0 = total * me / n_cta, u1 = total * min(me + 1, (long long)n_cta) / n_cta;
+    const long long u0 = quot(total * me, n_cta), u1 = quot(total * min(me + 1, (long long)n_cta), n_cta);
     long long u = u0;
     int s = 0;
     {
@@ -507,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dense_kernel(const __grid_c
         const int groups = (v.len + kGroup - 1) / kGroup;
         const int tiles = (v.n * P.group + 8 * NT - 1) / (8 * NT);
         const long long rem = u - pre[s];
-        const int in_seq = (int)(rem / groups), ga = (int)(rem % groups);
+        const int in_seq = (int)quot(rem, groups), ga = (int)(rem - (long long)in_seq * groups);
         const int gb = (int)min((long long)groups, ga + (u1 - u));
         Item it;
         it.seq = s;
@@ -530,7 +546,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dense_kernel(const __grid_c
 // empty), item after item; an item is a (token, kv-head, row tile).  CTA c of C takes
 // units [U c / C, U (c + 1) / C); with a CTA to each item, that is its list.
 template <class Ty, int NT>
-__global__ void __launch_bounds__(kThreads, 2) paged_sparse_kernel(const __grid_constant__ StreamParams SP) {
+__global__ void __launch_bounds__(Shape<NT>::kThreads, 2)
+    paged_sparse_kernel(const __grid_constant__ StreamParams SP) {
+    constexpr int kWarps = Shape<NT>::kWarps, kThreads = Shape<NT>::kThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_1k(smem_raw);
     float *sm_o = reinterpret_cast<float *>(smem);
@@ -539,14 +557,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_sparse_kernel(const __grid_
     const PagedAttnParams &P = SP.a;
     const PagedSeqs &S = P.seqs;
     WaitCtl wc;
-    Ring ring = ring_init(smem, wc, SP);
+    Ring ring = ring_init<NT>(smem, wc, SP);
     launch_dependents();
     const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
     const long long total = (long long)S.total * P.hkv * tiles * P.topk;
-    const long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+    const long long u0 = quot(total * blockIdx.x, gridDim.x), u1 = quot(total * (blockIdx.x + 1), gridDim.x);
     const int gp = S.page >> 4;
     for (long long u = u0; u < u1;) {
-        const int item = (int)(u / P.topk), a = (int)(u % P.topk);
+        const int item = (int)quot(u, P.topk), a = (int)(u - (long long)item * P.topk);
         const int b = (int)min((long long)P.topk, a + (u1 - u));
         const int slot = a == 0 && b == P.topk ? -1 : 2 * (int)blockIdx.x + (u == u0 ? 0 : 1);
         u += b - a;
@@ -586,7 +604,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_sparse_kernel(const __grid_
 // parts an item has follows from its units and the shares, as the kernel before cut
 // them.
 template <class Ty, int NT, bool kSparse>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams P) {
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedAttnParams P) {
+    constexpr int kWarps = kJoinWarps, kThreads = 32 * kJoinWarps;
     __shared__ float4 so[kWarps][32];
     __shared__ float sl[kWarps];
     const PagedSeqs &S = P.seqs;
@@ -625,10 +644,10 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
         n_cta = dense_ctas(total);
     }
     // CTA c holds units total c / n_cta .. total (c + 1) / n_cta - 1
-    const int c0 = (int)(((first + 1) * n_cta - 1) / total), c1 = (int)(((first + units) * n_cta - 1) / total);
+    const int c0 = (int)quot((first + 1) * n_cta - 1, total), c1 = (int)quot((first + units) * n_cta - 1, total);
     if (c0 == c1) return;  // whole, already written
     const int n_part = c1 - c0 + 1;
-    const int slot0 = 2 * c0 + (first == total * c0 / n_cta ? 0 : 1);
+    const int slot0 = 2 * c0 + (first == quot(total * c0, n_cta) ? 0 : 1);
     auto slot_of = [&](int i) -> size_t { return (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * 8 * NT + row; };
     float m = -INFINITY;
     for (int i = lane; i < n_part; i += 32) m = fmaxf(m, P.part_ml[slot_of(i)].x);
@@ -681,11 +700,11 @@ cudaError_t launch_dense(const StreamParams &SP, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int rt = (S.max_q * P.group + 8 * NT - 1) / (8 * NT);
     ProfScope prof("paged_dense", st);
-    paged_dense_kernel<Ty, NT><<<kStreamGrid, kThreads, bytes, st>>>(SP);
+    paged_dense_kernel<Ty, NT><<<kStreamGrid, Shape<NT>::kThreads, bytes, st>>>(SP);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_after(paged_join_kernel<Ty, NT, false>,
-                        dim3(S.n_seqs * P.hkv * rt, min(8 * NT, S.max_q * P.group)), dim3(kThreads), 0, st, P);
+                        dim3(S.n_seqs * P.hkv * rt, min(8 * NT, S.max_q * P.group)), dim3(32 * kJoinWarps), 0, st, P);
 }
 
 template <class Ty, int NT>
@@ -699,11 +718,10 @@ cudaError_t launch_sparse(const StreamParams &SP, cudaStream_t st) {
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(paged_sparse_kernel<Ty, NT>), bytes, done);
     if (e != cudaSuccess) return e;
     ProfScope prof("paged_sparse", st);
-    paged_sparse_kernel<Ty, NT><<<ctas, kThreads, bytes, st>>>(SP);
+    paged_sparse_kernel<Ty, NT><<<ctas, Shape<NT>::kThreads, bytes, st>>>(SP);
     e = cudaGetLastError();
     if (e != cudaSuccess || P.n_slots == 0) return e;
-    return launch_after(paged_join_kernel<Ty, NT, true>, dim3((unsigned)items, min(8 * NT, P.group)), dim3(kThreads), 0,
-                        st, P);
+    return launch_after(paged_join_kernel<Ty, NT, true>, dim3((unsigned)items, min(8 * NT, P.group)), dim3(32 * kJoinWarps), 0, st, P);
 }
 
 cudaError_t stream_maps(StreamParams &SP, const PagedAttnParams &P, bool fp16) {
@@ -723,10 +741,10 @@ StreamPlan paged_sparse_plan(int total, int hkv, int group, int topk, int page) 
     const int rows = group <= 8 ? 8 : 16;
     const long long items = (long long)total * hkv * ((group + rows - 1) / rows);
     // From four waves of items on, a CTA to each (their pages meet in L2 while neighbouring
-    // tokens run side by side); below, equal shares of one wave, of a 16-key group to a
-    // warp at least.
+    // tokens run side by side); below, equal shares of one wave, of four 16-key groups
+    // at least.
     if (items >= 4 * kStreamGrid) return {rows, 0};
-    const long long shares = std::min<long long>({kStreamGrid, items * topk, items * topk * page / (kGroup * kWarps)});
+    const long long shares = std::min<long long>({kStreamGrid, items * topk, items * topk * page / (4 * kGroup)});
     return {rows, 2 * (int)std::max(1ll, shares)};
 }
 
