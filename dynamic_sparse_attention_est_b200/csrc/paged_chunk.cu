@@ -103,33 +103,49 @@ __device__ __forceinline__ int seq_parts(int ktiles, int part_len) {
 // time for its prologue and epilogue, four more for the traffic of its partial
 // result (256 KB written and read); candidates whose cut units exceed the
 // partial slots are out.  Every CTA computes the same result.
-__device__ int choose_part_len(const ChunkParams &P, int *len_sh) {
+struct PlanSum {
+    long long units, cut;
+    float work;
+};
+__device__ int choose_part_len(const ChunkParams &P, PlanSum (*sum)[32], int *len_sh) {
     const PagedSeqs &S = P.a.seqs;
+    constexpr int kWarps = kThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int kt_max = 1;
+    for (int s = threadIdx.x; s < S.n_seqs; s += kThreads) {
+        const SeqView v = seq_view(S, s, P.a.hdr);
+        if (v.n > 0) kt_max = max(kt_max, seq_ktiles(v));
+    }
+    kt_max = __reduce_max_sync(0xffffffffu, kt_max);
+    if (lane == 0) sum[warp][0].units = kt_max;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) kt_max = max(kt_max, (int)sum[w][0].units);
+    __syncthreads();
+    // lane = candidate, each warp its share of the sequences
+    const int len = (kt_max + lane) / (lane + 1);
+    PlanSum mine{0, 0, 0.f};
+    for (int s = warp; s < S.n_seqs; s += kWarps) {
+        const SeqView v = seq_view(S, s, P.a.hdr);
+        if (v.n == 0) continue;
+        const int kt = seq_ktiles(v), parts = seq_parts(kt, len);
+        const long long items = (long long)P.a.hkv * seq_pairs(v, P.tpt);
+        mine.units += items * parts;
+        if (parts > 1) mine.cut += items * parts;
+        mine.work += (float)items * (float)kt;
+    }
+    sum[warp][lane] = mine;
+    __syncthreads();
     if (warp == 0) {
-        int kt_max = 1;
-        for (int s = lane; s < S.n_seqs; s += 32) {
-            const SeqView v = seq_view(S, s, P.a.hdr);
-            if (v.n > 0) kt_max = max(kt_max, seq_ktiles(v));
-        }
-        kt_max = __reduce_max_sync(0xffffffffu, kt_max);
-        const int len = (kt_max + lane) / (lane + 1);
-        long long units = 0, cut = 0;
-        float work = 0.f;
-        for (int s = 0; s < S.n_seqs; ++s) {
-            const SeqView v = seq_view(S, s, P.a.hdr);
-            if (v.n == 0) continue;
-            const int kt = seq_ktiles(v), parts = seq_parts(kt, len);
-            const long long items = (long long)P.a.hkv * seq_pairs(v, P.tpt);
-            units += items * parts;
-            if (parts > 1) cut += items * parts;
-            work += (float)items * (float)kt;
+        for (int w = 1; w < kWarps; ++w) {
+            mine.units += sum[w][lane].units;
+            mine.cut += sum[w][lane].cut;
+            mine.work += sum[w][lane].work;
         }
         float cost = INFINITY;
-        if (cut <= P.max_slots && units > 0) {
-            const float avg = work / (float)units;
-            const float rounds = (float)((units + kGrid - 1) / kGrid);
-            cost = rounds * (avg + (cut > 0 ? 6.f : 2.f)) + fmaxf(0.f, (float)len - avg);
+        if (mine.cut <= P.max_slots && mine.units > 0) {
+            const float avg = mine.work / (float)mine.units;
+            const float rounds = (float)((mine.units + kGrid - 1) / kGrid);
+            cost = rounds * (avg + (mine.cut > 0 ? 6.f : 2.f)) + fmaxf(0.f, (float)len - avg);
         }
         float best = cost;
 #pragma unroll
@@ -224,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         tmem_relinquish();
     }
     // ---- plan: part length, then per sequence the units and partial slots before it
-    const int part_len = choose_part_len(P, len_sh);
+    const int part_len =
+        choose_part_len(P, reinterpret_cast<PlanSum(*)[32]>(smem + kSmemRing), len_sh);  // the ring is not in use yet
     {
         const int per = (S.n_seqs + kThreads - 1) / kThreads;
         const int sa = min((int)threadIdx.x * per, S.n_seqs), sb = min(sa + per, S.n_seqs);
@@ -265,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         if (threadIdx.x == kThreads - 1) pre[S.n_seqs] = at;
     }
+    fence_proxy_async_smem();  // the plan's sums lay where the first loads go
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
     if (tid == 0) sh.seq = -1;
     __syncthreads();
     for (int s = tid; s < P.seqs.n_seqs; s += kSelectThreads)
-        if (seq_of(P.seqs, P.t0 + (int)blockIdx.x / P.hkv, s) >= 0) sh.seq = s;
+        if (seq_of(P.seqs, P.t0 + (int)blockIdx.x / P.hkv, s) >= 0) atomicMax(&sh.seq, s);
     __syncthreads();
     Row w;
     if (!row_setup(P, blockIdx.x, sh.seq, tid, kSelectThreads, w)) return;

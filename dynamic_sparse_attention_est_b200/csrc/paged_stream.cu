@@ -559,6 +559,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 2)
     WaitCtl wc;
     Ring ring = ring_init<NT>(smem, wc, SP);
     launch_dependents();
+    if (blockIdx.x == 0)  // no row leads to a sequence that ends before it begins: report it here
+        for (int s = threadIdx.x; s < S.n_seqs; s += kThreads) seq_view(S, s, P.hdr);
     const int tiles = (P.group + 8 * NT - 1) / (8 * NT);
     const long long total = (long long)S.total * P.hkv * tiles * P.topk;
     const long long u0 = quot(total * blockIdx.x, gridDim.x), u1 = quot(total * (blockIdx.x + 1), gridDim.x);
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 2)
         if (threadIdx.x == 0) found = -1;
         __syncthreads();
         for (int s = threadIdx.x; s < S.n_seqs; s += kThreads)
-            if (__ldg(S.cu_q + s) <= t && t < __ldg(S.cu_q + s + 1)) found = s;
+            if (__ldg(S.cu_q + s) <= t && t < __ldg(S.cu_q + s + 1)) atomicMax(&found, s);
         __syncthreads();
         const int s = found;
         __syncthreads();        // read by all before it is set again

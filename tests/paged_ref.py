@@ -169,3 +169,9 @@ def rotate(x, table, pos, rot, interleaved):
     mag[..., i], mag[..., j] = (a * c).abs() + (b * s).abs(), (b * c).abs() + (a * s).abs()
     # two products and a sum in fp32, then half a step of the result (fp16: or of its smallest)
     return y, u(x.dtype) * y.abs() + 3 * 2 ** -24 * mag * (1 + u(x.dtype)) + 2 ** -25
+
+
+def rope_table(n, rot, dev="cuda"):
+    inv = 500000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    ang = torch.arange(n, dtype=torch.float64)[:, None] * inv
+    return torch.cat([ang.cos(), ang.sin()], 1).float().to(dev)

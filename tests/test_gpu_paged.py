@@ -13,10 +13,7 @@ SCALE = 1.0 / math.sqrt(128)
 BF, HF = torch.bfloat16, torch.float16
 
 
-def rope_table(n, rot, dev="cuda"):
-    inv = 500000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
-    ang = torch.arange(n, dtype=torch.float64)[:, None] * inv
-    return torch.cat([ang.cos(), ang.sin()], 1).float().to(dev)
+rope_table = ref.rope_table
 
 
 # ------------------------------------------------------------------ append
