@@ -10,13 +10,16 @@
 // keeps its own page and the topk - 1 best earlier ones, ties to the lower page.
 //
 // Two kernels:
-//   scores  bound by reading the bounds (512 B per page and kv-head) for single
-//           tokens, by the matrix instructions for chunks.  16 pages are the rows
-//           of an m16n8k16 product; each warp brings its own pages in through a ring
-//           of bulk copies, one per page, at a stride of 528 B that ldmatrix reads
-//           without bank conflicts.  The columns are four tokens' Q, each as the sum
-//           of two 16-bit parts, which carries Q to 2^-16.  The scores are
-//           approximate, with a bound E on their error.
+//   scores  a product of pages by tokens, Q as the sum of two 16-bit parts, which
+//           carries it to 2^-16: approximate, with a bound E on the error.  Up to
+//           four new tokens: bound by reading the bounds (512 B per page and
+//           kv-head); 16 pages are the rows of an m16n8k16 product, whose columns
+//           are the four tokens' parts; each warp brings its own pages in through a
+//           ring of bulk copies, one per page, at a stride of 528 B that ldmatrix
+//           reads without bank conflicts.  Chunks: 128 pages by 64 tokens' parts on
+//           the tensor cores (tcgen05, K = 256), pages gathered by cp.async into the
+//           swizzled layout.  (mma.sync there took 29.5 us for 512 tokens over 1,016
+//           pages and eight kv-heads, at about a tenth of the tensor cores' rate.)
 //   select  one warp (many rows) or one CTA (few) per row: the k-th largest
 //           approximate score t by counting over a shrinking range of its key bits
 //           until few keys are left, which are ranked; then every page within 2 E of
@@ -55,6 +58,19 @@ __device__ __forceinline__ float part_scale<Fp16>(float top) {
     return ldexpf(1.f, min(14 - e, 100));
 }
 
+template <class Ty>
+__device__ __forceinline__ void add_signed(const uint4 &w, float (&up)[8], float (&down)[8]) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = Ty::unpack(x[i]);
+        up[2 * i] += fmaxf(f.x, 0.f);
+        up[2 * i + 1] += fmaxf(f.y, 0.f);
+        down[2 * i] += fminf(f.x, 0.f);
+        down[2 * i + 1] += fminf(f.y, 0.f);
+    }
+}
+
 // Q+ and Q- of channels 8 c .. 8 c + 7 of a token, fp32 (all terms of one sign).
 template <class Ty>
 __device__ __forceinline__ void q_sums(const EstimateParams &P, int tok, int h, int c, float (&up)[8], float (&down)[8]) {
@@ -63,17 +79,32 @@ __device__ __forceinline__ void q_sums(const EstimateParams &P, int tok, int h, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) up[i] = down[i] = 0.f;
 #pragma unroll 4
-    for (int g = 0; g < P.group; ++g) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(q + (long long)g * P.q_hs));
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    for (int g = 0; g < P.group; ++g)
+        add_signed<Ty>(__ldg(reinterpret_cast<const uint4 *>(q + (long long)g * P.q_hs)), up, down);
+}
+
+// The scale of a token's parts (sixteen lanes hold its sums): 1, or for fp16 the
+// power of two that suits its largest.
+template <class Ty>
+__device__ __forceinline__ float row_scale(const float (&up)[8], const float (&down)[8]) {
+    if (Ty::kIdescType != 0) return 1.f;  // bf16
+    float mx = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = Ty::unpack(x[i]);
-            up[2 * i] += fmaxf(f.x, 0.f);
-            up[2 * i + 1] += fmaxf(f.y, 0.f);
-            down[2 * i] += fminf(f.x, 0.f);
-            down[2 * i + 1] += fminf(f.y, 0.f);
-        }
+    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fmaxf(up[i], -down[i]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    return part_scale<Ty>(mx);
+}
+
+// x sc as the sum of two 16-bit parts.
+template <class Ty>
+__device__ __forceinline__ void two_parts(const float (&x)[8], float sc, uint32_t (&hi)[4], uint32_t (&mid)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = x[2 * i] * sc, b = x[2 * i + 1] * sc;
+        hi[i] = Ty::pack(a, b);
+        const float2 f = Ty::unpack(hi[i]);
+        mid[i] = Ty::pack(a - f.x, b - f.y);
     }
 }
 
@@ -85,22 +116,22 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
 
 // ------------------------------------------------------------------ scores
 // grid: x = sequence * tiles + token tile, y = kv-head, z = page range.
-template <int NT>
+constexpr int kTokSmall = 4, kTokLarge = 64;  // tokens of a tile
+
 struct ScoreShape {
-    static constexpr int kWarps = NT == 1 ? 6 : 4, kThreads = 32 * kWarps, kStages = 2;
+    static constexpr int kWarps = 6, kThreads = 32 * kWarps, kStages = 2;
     static constexpr uint32_t kRing = kWarps * kStages * kStepBytes;
-    static constexpr uint32_t kFrag = NT * 8 * 32 * 16;
+    static constexpr uint32_t kFrag = 8 * 32 * 16;
     static constexpr uint32_t kBytes = kRing + kFrag + 192;
 };
 
-template <class Ty, int NT>
-__global__ void __launch_bounds__(ScoreShape<NT>::kThreads, 2)
-    paged_scores_kernel(const __grid_constant__ EstimateParams P) {
+template <class Ty>
+__global__ void __launch_bounds__(ScoreShape::kThreads, 2) paged_scores_kernel(const __grid_constant__ EstimateParams P) {
     using T = typename Ty::T;
-    using Shape = ScoreShape<NT>;
-    constexpr int kTok = 4 * NT, kStages = Shape::kStages, kWarps = Shape::kWarps;
+    using Shape = ScoreShape;
+    constexpr int kTok = kTokSmall, kStages = Shape::kStages, kWarps = Shape::kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint4 *qf = reinterpret_cast<uint4 *>(smem + Shape::kRing);  // column fragments [NT][8][32]
+    uint4 *qf = reinterpret_cast<uint4 *>(smem + Shape::kRing);  // column fragments [8][32]
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Shape::kRing + Shape::kFrag);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + kWarps * kStages);
     float *warp_top = reinterpret_cast<float *>(bars + kWarps * kStages + 1);
@@ -145,44 +176,29 @@ __global__ void __launch_bounds__(ScoreShape<NT>::kThreads, 2)
     for (int st = 0; st < kStages; ++st)
         if (first + st * kStride < pb) fill(st, id[st]);
 
-    // column fragments: column n of tile nt is part n & 1 of token 4 nt + n / 2; sixteen
-    // threads a token, 8 channels each, element = side * 128 + channel
-    {
-        constexpr int kPass = Shape::kThreads / 16;
-        const int ch = threadIdx.x & 15;
+    // column fragments: column n is part n & 1 of token n / 2; sixteen threads a token,
+    // 8 channels each, element = side * 128 + channel
+    if (threadIdx.x < 16 * kTok) {
+        const int ch = threadIdx.x & 15, x = threadIdx.x >> 4;
+        float up[8] = {}, down[8] = {};
+        if (ta + x < tb) q_sums<Ty>(P, ta + x, h, ch, up, down);
+        const float sc = row_scale<Ty>(up, down);
 #pragma unroll
-        for (int x0 = 0; x0 < (kTok + kPass - 1) / kPass; ++x0) {
-            const int x = x0 * kPass + (threadIdx.x >> 4);
-            if (x >= kTok) break;  // whole warps: kTok is a multiple of 4
-            float up[8] = {}, down[8] = {};
-            if (ta + x < tb) q_sums<Ty>(P, ta + x, h, ch, up, down);
-            float sc = 1.f;
-            if (Ty::kIdescType == 0) {  // fp16: scaled by the row's largest
-                float mx = 0.f;
+        for (int side = 0; side < 2; ++side) {
+            // element side * 128 + 8 ch + 2 p: k-step / 16, register (/ 8) % 2, lane column p
+            const int kk = side * 8 + (ch >> 1), reg = (kk & 1) * 2 + (ch & 1);
+            uint32_t hi[4], mid[4];
+            two_parts<Ty>(side ? up : down, sc, hi, mid);
+            uint32_t *w = reinterpret_cast<uint32_t *>(qf + (kk >> 1) * 32);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fmaxf(up[i], -down[i]));
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                sc = part_scale<Ty>(mx);
-            }
-#pragma unroll
-            for (int side = 0; side < 2; ++side) {
-                // element e = side * 128 + 8 ch + 2 p: k-step e / 16, register (e / 8) % 2, lane column p
-                const int kk = side * 8 + (ch >> 1), reg = (kk & 1) * 2 + (ch & 1);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const float a = (side ? up : down)[2 * p] * sc, b = (side ? up : down)[2 * p + 1] * sc;
-                    const uint32_t hi = Ty::pack(a, b);
-                    const float2 f = Ty::unpack(hi);
-                    const uint32_t mid = Ty::pack(a - f.x, b - f.y);
-                    uint32_t *w = reinterpret_cast<uint32_t *>(qf + ((x >> 2) * 8 + (kk >> 1)) * 32);
-                    w[((2 * (x & 3)) * 4 + p) * 4 + reg] = hi;
-                    w[((2 * (x & 3) + 1) * 4 + p) * 4 + reg] = mid;
-                }
+            for (int p = 0; p < 4; ++p) {
+                w[((2 * x) * 4 + p) * 4 + reg] = hi[p];
+                w[((2 * x + 1) * 4 + p) * 4 + reg] = mid[p];
             }
         }
     }
     __syncthreads();
+    launch_dependents();  // the selection's own preparations run beside the rest of this
 
     int st = 0;
     uint32_t phase = 0;
@@ -226,30 +242,17 @@ __global__ void __launch_bounds__(ScoreShape<NT>::kThreads, 2)
             lo2 = Ty::vmin(lo2, l1);
             hi2 = Ty::vmax(hi2, h1);
         }
-        // two token tiles at a time: four chains of products
-        constexpr int kPair = NT == 1 ? 1 : 2;
+        float d[2][4] = {};
 #pragma unroll
-        for (int t = 0; t < NT; t += kPair) {
-            if (4 * t < tb - ta) {
-                float d[kPair][2][4] = {};
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int y = 0; y < kPair; ++y) {
-                        const uint4 b = qf[((t + y) * 8 + i) * 32 + lane];
-                        Ty::mma(d[y][0], a[2 * i][0], a[2 * i][1], a[2 * i][2], a[2 * i][3], b.x, b.y);
-                        Ty::mma(d[y][1], a[2 * i + 1][0], a[2 * i + 1][1], a[2 * i + 1][2], a[2 * i + 1][3], b.z, b.w);
-                    }
-#pragma unroll
-                for (int y = 0; y < kPair; ++y) {
-                    const int tok = ta + 4 * (t + y) + c;
-                    if (tok < tb) {
-                        float *dst = P.scores + ((long long)(tok - P.t0) * P.hkv + h) * P.score_stride + j0 + r;
-                        if (r0) dst[0] = (d[y][0][0] + d[y][1][0]) + (d[y][0][1] + d[y][1][1]);
-                        if (r1) dst[8] = (d[y][0][2] + d[y][1][2]) + (d[y][0][3] + d[y][1][3]);
-                    }
-                }
-            }
+        for (int i = 0; i < 8; ++i) {
+            const uint4 b = qf[i * 32 + lane];
+            Ty::mma(d[0], a[2 * i][0], a[2 * i][1], a[2 * i][2], a[2 * i][3], b.x, b.y);
+            Ty::mma(d[1], a[2 * i + 1][0], a[2 * i + 1][1], a[2 * i + 1][2], a[2 * i + 1][3], b.z, b.w);
+        }
+        if (ta + c < tb) {
+            float *dst = P.scores + ((long long)(ta + c - P.t0) * P.hkv + h) * P.score_stride + j0 + r;
+            if (r0) dst[0] = (d[0][0] + d[1][0]) + (d[0][1] + d[1][1]);
+            if (r1) dst[8] = (d[0][2] + d[1][2]) + (d[0][3] + d[1][3]);
         }
     }
     // largest |bound| of this tile's page range
@@ -266,7 +269,182 @@ __global__ void __launch_bounds__(ScoreShape<NT>::kThreads, 2)
             P.top[((long long)blockIdx.x * P.hkv + h) * gridDim.z + blockIdx.z] = fmaxf(top, 0.f);
         }
     }
-    launch_dependents();
+}
+
+// Chunks: 128 pages (rows, K-major in 128-byte swizzle: four 64-channel pieces of 16
+// KB) by 64 tokens' two parts (128 rows alike), K = 256.  Two page tiles in shared
+// memory: while the tensor cores multiply one, the next is on its way.
+constexpr int kTcThreads = 256, kPageTile = 128;
+constexpr uint32_t kPieceBytes = 16384, kTileBytes = 4 * kPieceBytes;
+constexpr uint32_t kTcBar = 3 * kTileBytes;  // two page tiles, the token tile
+constexpr uint32_t kTcBytes = kTcBar + 128 + 1024;
+
+template <class Ty>
+__global__ void __launch_bounds__(kTcThreads, 1) paged_scores_tc_kernel(const __grid_constant__ EstimateParams P) {
+    using T = typename Ty::T;
+    extern __shared__ uint8_t tc_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(tc_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sA = smem_u32(smem), sB = sA + 2 * kTileBytes;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kTcBar);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bar + 1);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 2);
+    float *warp_top = reinterpret_cast<float *>(bar + 3);  // [8]
+    const PagedSeqs &S = P.seqs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = blockIdx.x / P.tiles, h = blockIdx.y;
+    const SeqView v = seq_view(S, s, P.hdr);
+    const int ta = max(v.q0, P.t0) + (int)(blockIdx.x % P.tiles) * kTokLarge;
+    const int tb = min(min(v.q0 + v.n, P.t1), ta + kTokLarge);
+    if (ta >= tb) return;
+    const int last_pos = v.len - v.n + (tb - 1 - v.q0);
+    const int n_pages = last_pos < 0 ? 0 : last_pos >> S.page_log2;  // pages before the last token's own
+    const int pa = blockIdx.z * P.pages_per_cta, pb = min(pa + P.pages_per_cta, n_pages);
+    if (pa >= pb) return;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(bar), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_slot), 128);
+        tmem_relinquish();
+    }
+    const WaitCtl wc{abort_flag, &P.hdr->status, P.wait_limit_ns};
+
+    // a warp brings in 16 pages, a lane 16 bytes of each: lanes 0 - 15 min, 16 - 31 max
+    const int side = lane >> 4;
+    const T *kb = static_cast<const T *>(P.bounds) + (long long)h * 2 * kD + lane * 8;
+    const long long page_stride = (long long)P.hkv * 2 * kD;
+    auto id_at = [&](int j0) -> int {  // lane i: page id of the warp's row i
+        const int j = j0 + warp * 16 + lane;
+        return lane < 16 && j < pb ? page_of(S, s, j, P.hdr) : -1;
+    };
+    auto piece = [&](int i) -> uint32_t {  // shared offset of the lane's 16 bytes of the warp's row i
+        const int row = warp * 16 + i;
+        return (lane >> 3) * kPieceBytes + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+    };
+    auto fill = [&](int st, int ids) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int id = __shfl_sync(0xffffffffu, ids, i);
+            if (id >= 0) cp_async16(sA + st * kTileBytes + piece(i), kb + id * page_stride);
+        }
+    };
+    int id = id_at(pa), id_next = id_at(pa + kPageTile);
+    fill(0, id);
+    // The tokens' parts: row 2 x + part; sixteen threads a token, 8 channels each, the
+    // loads of all its four tokens in flight together.
+    {
+        constexpr int kPass = kTokLarge * 16 / kTcThreads;
+        const int ch = threadIdx.x & 15, x0 = threadIdx.x >> 4;
+        float up[kPass][8] = {}, down[kPass][8] = {};
+        const T *q = static_cast<const T *>(P.q) + (long long)(ta + x0) * P.q_ts + (long long)h * P.group * P.q_hs + ch * 8;
+        for (int g0 = 0; g0 < P.group; g0 += 4) {
+            uint4 w[kPass][4];
+#pragma unroll
+            for (int x = 0; x < kPass; ++x)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    w[x][g] = ta + x0 + 16 * x < tb && g0 + g < P.group
+                                  ? __ldg(reinterpret_cast<const uint4 *>(q + (long long)(16 * x) * P.q_ts +
+                                                                          (long long)(g0 + g) * P.q_hs))
+                                  : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < kPass; ++x)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) add_signed<Ty>(w[x][g], up[x], down[x]);
+        }
+#pragma unroll
+        for (int y = 0; y < kPass; ++y) {
+            const int x = x0 + 16 * y;
+            const float sc = row_scale<Ty>(up[y], down[y]);
+#pragma unroll
+            for (int sd = 0; sd < 2; ++sd) {
+                uint32_t hi[4], mid[4];
+                two_parts<Ty>(sd ? up[y] : down[y], sc, hi, mid);
+                uint8_t *dst = smem + 2 * kTileBytes + (2 * sd + (ch >> 3)) * kPieceBytes;
+                const int r0 = 2 * x, r1 = 2 * x + 1, c16 = ch & 7;
+                *reinterpret_cast<uint4 *>(dst + r0 * 128 + ((c16 ^ (r0 & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(dst + r1 * 128 + ((c16 ^ (r1 & 7)) << 4)) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+            }
+        }
+    }
+    launch_dependents();  // the selection's own preparations run beside the rest of this
+    constexpr uint32_t kIdesc = (1u << 4) | Ty::kIdescType | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+    const uint64_t da = sdesc_sw128(sA, 16, 1024), db = sdesc_sw128(sB, 16, 1024);
+    uint32_t ext2 = side ? Ty::kNegInf2 : Ty::kPosInf2;  // largest max, or smallest min
+    int st = 0, par = 0;
+    bool ok = true;
+    for (int j0 = pa; j0 < pb; j0 += kPageTile) {
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();  // the tile is complete, and the products and reads of the one before are over
+        tc_fence_after();
+        const uint32_t tmem = *tmem_slot;
+        if (warp == 0) {
+            // K = 256 as two calls of eight K = 16 steps over two pieces each
+            const uint64_t a0 = da + (uint64_t)(st * (kTileBytes >> 4));
+            umma_ss_tile_warp(tmem, a0, db, kIdesc, 0u);
+            umma_ss_tile_warp(tmem, a0 + 2 * (kPieceBytes >> 4), db + 2 * (kPieceBytes >> 4), kIdesc, 1u);
+            umma_commit_warp(smem_u32(bar));
+        }
+        const int id_here = id;
+        id = id_next;
+        if (j0 + kPageTile < pb) {
+            fill(st ^ 1, id);
+            id_next = id_at(j0 + 2 * kPageTile);
+        }
+        // No key exceeds its page's max nor falls below its min, so the largest |bound| is
+        // the largest max or the largest -min.
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (__shfl_sync(0xffffffffu, id_here, i) >= 0) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(smem + st * kTileBytes + piece(i));
+                const uint32_t a = side ? Ty::vmax(Ty::vmax(w.x, w.y), Ty::vmax(w.z, w.w))
+                                        : Ty::vmin(Ty::vmin(w.x, w.y), Ty::vmin(w.z, w.w));
+                ext2 = side ? Ty::vmax(ext2, a) : Ty::vmin(ext2, a);
+            }
+        const bool got = wait_bounded(smem_u32(bar), par, wc, wait_site(9, 0, j0));
+        ok = !__syncthreads_or(!got);
+        if (!ok) break;
+        par ^= 1;
+        tc_fence_after();
+        // lane = page; a warp takes half of its quarter's columns: 32 tokens' pairs of parts
+        const int page = j0 + (warp & 3) * 32 + lane, t0 = ta + (warp >> 2) * 32;
+        const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (warp >> 2) * 64;
+        uint32_t d[2][32];
+        tmem_ld32(at, d[0]);
+        tmem_ld32(at + 32, d[1]);
+        tmem_ld_wait(d[0]);
+        tmem_ld_wait(d[1]);
+        const int n_tok = page < pb ? tb - t0 : 0;
+        const long long step = (long long)P.hkv * P.score_stride;
+        float *dst = P.scores + ((long long)(t0 - P.t0) * P.hkv + h) * P.score_stride + page;
+#pragma unroll
+        for (int y = 0; y < 32; ++y) {
+            if (y < n_tok) *dst = __uint_as_float(d[y >> 4][2 * (y & 15)]) + __uint_as_float(d[y >> 4][2 * (y & 15) + 1]);
+            dst += step;
+        }
+        st ^= 1;
+    }
+    cp_async_wait_all();  // none is in flight when the CTA exits
+    {
+        const float2 f = Ty::unpack(ext2);
+        float top = side ? fmaxf(f.x, f.y) : fmaxf(-f.x, -f.y);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) warp_top[warp] = top;
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int w = 0; w < kTcThreads / 32; ++w) top = fmaxf(top, warp_top[w]);
+            P.top[((long long)blockIdx.x * P.hkv + h) * gridDim.z + blockIdx.z] = fmaxf(top, 0.f);
+        }
+        if (warp == 0) tmem_dealloc(*tmem_slot, 128);
+    }
 }
 
 // ------------------------------------------------------------------ select
@@ -365,31 +543,31 @@ __device__ __forceinline__ int seq_of(const PagedSeqs &S, int tok, int s) {
     return s < S.n_seqs && __ldg(S.cu_q + s) <= tok && tok < __ldg(S.cu_q + s + 1) ? s : -1;
 }
 
-// Sixteen lanes: Q in 64 bits (8 channels a lane) to q (Q- then Q+), its 1-norm and
+// One warp: Q in 64 bits (4 channels a lane) to q (Q- then Q+), its 1-norm and
 // largest element in l1 and mx of each lane (the lane's own share).
 template <class Ty>
 __device__ __forceinline__ void exact_q(const EstimateParams &P, const Row &w, int lane, double *q, float &l1, float &mx) {
-    double up[8] = {}, down[8] = {};
+    double up[4] = {}, down[4] = {};
     const typename Ty::T *src = static_cast<const typename Ty::T *>(P.q) + (long long)w.tok * P.q_ts +
-                                (long long)w.h * P.group * P.q_hs + lane * 8;
+                                (long long)w.h * P.group * P.q_hs + lane * 4;
+#pragma unroll 4
     for (int g = 0; g < P.group; ++g) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + (long long)g * P.q_hs));
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + (long long)g * P.q_hs));
+        const float2 f0 = Ty::unpack(v.x), f1 = Ty::unpack(v.y);
+        const float f[4] = {f0.x, f0.y, f1.x, f1.y};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 f = Ty::unpack(x[i]);
-            up[2 * i] += (double)fmaxf(f.x, 0.f);
-            up[2 * i + 1] += (double)fmaxf(f.y, 0.f);
-            down[2 * i] += (double)fminf(f.x, 0.f);
-            down[2 * i + 1] += (double)fminf(f.y, 0.f);
+            const double d = (double)f[i];
+            up[i] += f[i] > 0.f ? d : 0.0;
+            down[i] += f[i] < 0.f ? d : 0.0;
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        q[lane * 8 + i] = down[i];
-        q[kD + lane * 8 + i] = up[i];
+    for (int i = 0; i < 4; ++i) {
+        q[lane * 4 + i] = down[i];
+        q[kD + lane * 4 + i] = up[i];
         l1 += (float)(up[i] - down[i]);
-        mx = fmaxf(mx, (float)fmax(up[i], -down[i]));
+        mx = fmaxf(mx, fmaxf((float)up[i], (float)-down[i]));
     }
 }
 
@@ -405,8 +583,12 @@ __device__ __forceinline__ float error_bound(const EstimateParams &P, float l1, 
 // either side (0.1 % wider: the roundings here).
 __device__ __forceinline__ void doubt_range(uint32_t t_key, float err, uint32_t &k_lo, uint32_t &k_hi) {
     const float t = from_key(t_key), width = 2.002f * err + 1e-6f * fabsf(t);
-    k_lo = order_key(t - width);
-    k_hi = order_key(t + width);
+    k_lo = max(order_key(t - width), 1u);
+    k_hi = min(order_key(t + width), 0xfffffffeu);
+    if (k_lo > t_key || k_hi < t_key) {  // infinities or NaN among the bounds: everything is in doubt
+        k_lo = 1u;
+        k_hi = 0xfffffffeu;
+    }
 }
 
 // Many pages in doubt (repeated pages): counts over the bits of their exact scores,
@@ -479,7 +661,7 @@ __global__ void __launch_bounds__(kSelectThreads, kPer == 32 ? 3 : 2)
     Row w;
     if (!row_setup(P, row_in, s, lane, 32, w)) return;
     float l1 = 0.f, mxq = 0.f, top = 0.f;
-    if (lane < 16) exact_q<Ty>(P, w, lane, sh.q, l1, mxq);
+    exact_q<Ty>(P, w, lane, sh.q, l1, mxq);
 #pragma unroll
     for (int e = 0; e < 64 / 32; ++e) sh.chosen[e * 32 + lane] = 0;
     wait_for_primary();  // the scores
@@ -565,24 +747,35 @@ __global__ void __launch_bounds__(kSelectThreads, kPer == 32 ? 3 : 2)
     }
     uint32_t k_lo, k_hi;
     doubt_range(lo, error_bound<Ty>(P, l1, mxq, top), k_lo, k_hi);
-    k_lo = max(k_lo, 1u);
-    unsigned n_hi = 0, n_in = 0;
+    // From here on bit sets: lane e (and 32 + e, kPer = 64) has the candidates 32 e ..
+    // 32 e + 31 that are taken for sure, and those in doubt.
+    constexpr int kSets = kPer / 32;
+    unsigned sure[kSets] = {}, doubt[kSets] = {};
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-        n_hi += key[e] > k_hi;
-        n_in += key[e] >= k_lo;
+        const unsigned a = __ballot_sync(0xffffffffu, key[e] > k_hi), b = __ballot_sync(0xffffffffu, key[e] >= k_lo);
+        if (lane == (e & 31)) {
+            sure[e >> 5] = a;
+            doubt[e >> 5] = b & ~a;
+        }
+    }
+    unsigned n_hi = 0, n_in = 0;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) {
+        n_hi += __popc(sure[i]);
+        n_in += __popc(doubt[i]);
     }
     n_hi = __reduce_add_sync(0xffffffffu, n_hi);
-    n_in = __reduce_add_sync(0xffffffffu, n_in) - n_hi;
+    n_in = __reduce_add_sync(0xffffffffu, n_in);
     const unsigned want = w.take - n_hi;  // of the pages in doubt
-    const bool open = n_in != want;
-    if (open) {
+    if (n_in != want) {
         if (lane == 0) sh.n_border = 0;
         __syncwarp();
         if (n_in <= kWarpBorder) {
 #pragma unroll
-            for (int e = 0; e < kPer; ++e)
-                if (key[e] - k_lo <= k_hi - k_lo) sh.border[atomicAdd(&sh.n_border, 1u)] = e * 32 + lane;  // any order
+            for (int i = 0; i < kSets; ++i)
+                for (unsigned m = doubt[i]; m; m &= m - 1)
+                    sh.border[atomicAdd(&sh.n_border, 1u)] = (i * 32 + lane) * 32 + __ffs(m) - 1;  // any order
             __syncwarp();
             for (unsigned i0 = 0; i0 < n_in; i0 += 4) {
                 const unsigned i = i0 + (lane >> 3);
@@ -608,16 +801,23 @@ __global__ void __launch_bounds__(kSelectThreads, kPer == 32 ? 3 : 2)
                 });
         }
         __syncwarp();
-    }
-    unsigned to = 0;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const bool doubt = key[e] >= k_lo && key[e] <= k_hi;
-        const bool yes = key[e] > k_hi || (doubt && (!open || (sh.chosen[e] >> lane) & 1u));
-        const unsigned bal = __ballot_sync(0xffffffffu, yes);
-        const unsigned at = to + __popc(bal & ((1u << lane) - 1u));
-        if (yes && at < (unsigned)w.take) w.out[at] = e * 32 + lane;
-        to += __popc(bal);
+        for (int i = 0; i < kSets; ++i) doubt[i] = sh.chosen[i * 32 + lane];
+    }
+    unsigned base = 0;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) {
+        unsigned m = sure[i] | doubt[i];
+        const unsigned n_mine = __popc(m);
+        unsigned inc = n_mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        for (unsigned at = base + inc - n_mine; m; m &= m - 1, ++at)
+            if (at < (unsigned)w.take) w.out[at] = (i * 32 + lane) * 32 + __ffs(m) - 1;
+        base += __shfl_sync(0xffffffffu, inc, 31);
     }
 }
 
@@ -671,7 +871,7 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
     if (!row_setup(P, blockIdx.x, sh.seq, tid, kSelectThreads, w)) return;
     if (warp == 0) {
         float l1 = 0.f, mxq = 0.f;
-        if (lane < 16) exact_q<Ty>(P, w, lane, sh.q, l1, mxq);
+        exact_q<Ty>(P, w, lane, sh.q, l1, mxq);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             l1 += __shfl_xor_sync(0xffffffffu, l1, o);
@@ -825,26 +1025,27 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
     }
 }
 
-constexpr int kTokSmall = 4, kTokLarge = 32;
-
 constexpr int kMaxRanges = 64;  // page ranges of a score launch
 
-template <class Ty, int NT>
-cudaError_t launch_scores(EstimateParams &P, cudaStream_t st) {
+template <class Ty>
+cudaError_t launch_scores(EstimateParams &P, bool small, cudaStream_t st) {
     const PagedSeqs &S = P.seqs;
-    static std::atomic<unsigned long long> done{0};
-    cudaError_t e = allow_smem(reinterpret_cast<const void *>(paged_scores_kernel<Ty, NT>), (int)ScoreShape<NT>::kBytes,
-                               done);
+    static std::atomic<unsigned long long> done_small{0}, done_tc{0};
+    cudaError_t e =
+        small ? allow_smem(reinterpret_cast<const void *>(paged_scores_kernel<Ty>), (int)ScoreShape::kBytes, done_small)
+              : allow_smem(reinterpret_cast<const void *>(paged_scores_tc_kernel<Ty>), (int)kTcBytes, done_tc);
     if (e != cudaSuccess) return e;
-    // page ranges: about two CTAs to an SM over all (sequence, tile, kv-head)s
+    // page ranges: one wave of CTAs over all (sequence, tile, kv-head)s
     const long long rows = (long long)S.n_seqs * P.tiles * P.hkv;
-    const int step = ScoreShape<NT>::kWarps * kStepPages;
-    const int most = (S.width + step - 1) / step;
-    const int z = (int)std::max<long long>(1, std::min<long long>({most, 296 / rows, kMaxRanges}));
-    P.pages_per_cta = ((S.width + z - 1) / z + step - 1) / step * step;
-    P.ranges = (S.width + P.pages_per_cta - 1) / P.pages_per_cta;
+    const int step = small ? ScoreShape::kWarps * kStepPages : kPageTile;
+    const int pages = std::max(1, S.width - 1);  // candidates: the token's own page is none
+    const int most = (pages + step - 1) / step;
+    const int z = (int)std::max<long long>(1, std::min<long long>({most, (small ? 296 : 148) / rows, kMaxRanges}));
+    P.pages_per_cta = (most + z - 1) / z * step;
+    P.ranges = (pages + P.pages_per_cta - 1) / P.pages_per_cta;
     const dim3 grid((unsigned)(S.n_seqs * P.tiles), P.hkv, P.ranges);
-    paged_scores_kernel<Ty, NT><<<grid, ScoreShape<NT>::kThreads, ScoreShape<NT>::kBytes, st>>>(P);
+    if (small) paged_scores_kernel<Ty><<<grid, ScoreShape::kThreads, ScoreShape::kBytes, st>>>(P);
+    else paged_scores_tc_kernel<Ty><<<grid, kTcThreads, kTcBytes, st>>>(P);
     return cudaGetLastError();
 }
 
@@ -852,7 +1053,7 @@ template <class Ty>
 cudaError_t launch_select(const EstimateParams &P, cudaStream_t st) {
     const int rows = (P.t1 - P.t0) * P.hkv;
     // A warp per row once the rows fill the SMs that way: 4,096 rows of 1,016 pages take
-    // 30 us so and 40 us with a CTA each.  128 rows of 2,048 pages take 13 us with a CTA each.
+    // 22 us so and 40 us with a CTA each; 128 rows of 2,048 pages 13 us with a CTA each.
     const int most = P.seqs.width - 1;  // candidates: the token's own page is none
     if (rows >= 1024 && most <= 2048) {
         const dim3 grid((rows + kSelectWarps - 1) / kSelectWarps);
@@ -881,7 +1082,7 @@ cudaError_t launch(EstimateParams P, cudaStream_t st) {
         const int tok = small ? kTokSmall : kTokLarge;
         P.tiles = (most + tok - 1) / tok;
         P.tile_tokens = tok;
-        cudaError_t e = small ? launch_scores<Ty, kTokSmall / 4>(P, st) : launch_scores<Ty, kTokLarge / 4>(P, st);
+        cudaError_t e = launch_scores<Ty>(P, small, st);
         if (e != cudaSuccess) return e;
         e = launch_select<Ty>(P, st);
         if (e != cudaSuccess) return e;

@@ -326,3 +326,22 @@ def test_estimate_decides_scores_that_differ_in_the_last_bits():
     idx, cnt = minf.minf_paged_block_estimate(c.q, kb, *c.meta(), page_size=16, topk=40)
     wi, wc = ref.estimate(c, kb, 40)
     assert torch.equal(cnt, wc) and torch.equal(idx, wi)
+
+
+@pytest.mark.parametrize("lens,pages", [([2], 60), ([300], 300), ([300], 1500)])
+@pytest.mark.parametrize("what", ["inf", "nan", "all_inf"])
+def test_estimate_stays_in_its_lists_whatever_the_bounds_hold(lens, pages, what):
+    """Bounds that are not finite: which pages are taken is unspecified, but the lists are lists of pages
+    before the token's own, ascending and distinct, with the own page last."""
+    c = ref.Case(lens, [16 * pages + lens[0]], 4, 2, 16, HF, seed=1)
+    kb = torch.nan_to_num(ref.bounds(c))
+    bad = {"inf": math.inf, "nan": math.nan, "all_inf": math.inf}[what]
+    if what == "all_inf":
+        kb[:, :, 1] = bad
+    else:
+        kb[::3, :, 1, 5] = bad
+    idx, cnt = minf.minf_paged_block_estimate(c.q, kb, *c.meta(), page_size=16, topk=20)
+    pos = torch.arange(c.kv[0] - lens[0], c.kv[0], device="cuda") // 16
+    assert (cnt <= 20).all() and (cnt >= 1).all()
+    own = idx.gather(2, (cnt - 1).long()[..., None])[..., 0]
+    assert torch.equal(own, pos[:, None].expand_as(own).int())
