@@ -439,6 +439,13 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
 }
 
 // ------------------------------------------------------------------ dense
+// 16-key groups of a sequence, over its kv-heads and row tiles.
+template <int NT>
+__device__ __forceinline__ long long seq_units(const SeqView &v, const PagedAttnParams &P) {
+    const int tiles = (v.n * P.group + 8 * NT - 1) / (8 * NT);
+    return (long long)tiles * P.hkv * ((v.len + kGroup - 1) / kGroup);
+}
+
 // Work units: 16-key groups, sequence after sequence; within one, (kv-head, row
 // tile) after one another.  CTA c of C takes units [U c / C, U (c + 1) / C).
 template <class Ty, int NT>
@@ -459,11 +466,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 2)
 
     const int per = (S.n_seqs + kThreads - 1) / kThreads;
     const int sa = min(threadIdx.x * per, S.n_seqs), sb = min(sa + per, S.n_seqs);
-    auto units = [&](int s) -> long long {
-        const SeqView v = seq_view(S, s, P.hdr);
-        const int tiles = (v.n * P.group + 8 * NT - 1) / (8 * NT);
-        return (long long)tiles * P.hkv * ((v.len + kGroup - 1) / kGroup);
-    };
+    auto units = [&](int s) { return seq_units<NT>(seq_view(S, s, P.hdr), P); };
     long long mine = 0;
     for (int s = sa; s < sb; ++s) mine += units(s);
     long long inc = mine;
@@ -602,14 +605,16 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 2)
 }
 
 // ------------------------------------------------------------------ join
-// One CTA per (item, row): the parts in order, a quarter of them to each warp.  Which
-// parts an item has follows from its units and the shares, as the kernel before cut
-// them.
+// One CTA per (item, row): the parts in order, a quarter of them to each warp, four in
+// flight.  Which parts an item has follows from its units and the shares, as the
+// kernel before cut them; all that needs no result of that kernel is done while it
+// still runs.
 template <class Ty, int NT, bool kSparse>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedAttnParams P) {
     constexpr int kWarps = kJoinWarps, kThreads = 32 * kJoinWarps;
     __shared__ float4 so[kWarps][32];
-    __shared__ float sl[kWarps];
+    __shared__ float2 sml[kWarps];
+    __shared__ long long sums[kWarps][2];
     const PagedSeqs &S = P.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int id = blockIdx.x, row = blockIdx.y;
@@ -630,7 +635,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
         first = (long long)id * units;
         total = (long long)S.total * P.hkv * tiles * units;
         n_cta = P.n_slots / 2;
-        wait_for_primary();
     } else {
         const int rt_max = (S.max_q * P.group + 8 * NT - 1) / (8 * NT);
         const int s = id / rt_max / P.hkv, rt = id % rt_max;
@@ -640,9 +644,33 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
         tok0 = v.q0;
         if (x >= v.n * P.group || v.len == 0) return;
         units = (v.len + kGroup - 1) / kGroup;
-        wait_for_primary();
-        total = P.plan[S.n_seqs];
-        first = P.plan[s] + (h * (long long)((v.n * P.group + 8 * NT - 1) / (8 * NT)) + rt) * units;
+        const long long before = (h * (long long)((v.n * P.group + 8 * NT - 1) / (8 * NT)) + rt) * units;
+        if (S.n_seqs <= kThreads) {
+            long long mine = 0;
+            if (threadIdx.x < S.n_seqs) mine = seq_units<NT>(seq_view(S, threadIdx.x, P.hdr), P);
+            long long head = threadIdx.x < s ? mine : 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                mine += __shfl_xor_sync(0xffffffffu, mine, o);
+                head += __shfl_xor_sync(0xffffffffu, head, o);
+            }
+            if (lane == 0) {
+                sums[warp][0] = mine;
+                sums[warp][1] = head;
+            }
+            __syncthreads();
+            total = first = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                total += sums[w][0];
+                first += sums[w][1];
+            }
+        } else {
+            wait_for_primary();
+            total = P.plan[S.n_seqs];
+            first = P.plan[s];
+        }
+        first += before;
         n_cta = dense_ctas(total);
     }
     // CTA c holds units total c / n_cta .. total (c + 1) / n_cta - 1
@@ -650,37 +678,46 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
     if (c0 == c1) return;  // whole, already written
     const int n_part = c1 - c0 + 1;
     const int slot0 = 2 * c0 + (first == quot(total * c0, n_cta) ? 0 : 1);
-    auto slot_of = [&](int i) -> size_t { return (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * 8 * NT + row; };
-    float m = -INFINITY;
-    for (int i = lane; i < n_part; i += 32) m = fmaxf(m, P.part_ml[slot_of(i)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f;
+    wait_for_primary();
+    float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = warp; i < n_part; i += kWarps) {
-        const size_t si = slot_of(i);
-        const float2 ml = P.part_ml[si];
-        const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-        const float4 o = reinterpret_cast<const float4 *>(P.part_o)[si * 32 + lane];
-        l = fmaf(ml.y, a, l);
+    auto add = [&](float a, float pl, const float4 &o) {
+        l = fmaf(pl, a, l);
         acc.x = fmaf(o.x, a, acc.x);
         acc.y = fmaf(o.y, a, acc.y);
         acc.z = fmaf(o.z, a, acc.z);
         acc.w = fmaf(o.w, a, acc.w);
+    };
+    auto raise = [&](float top) {  // m to a larger maximum
+        const float a = m == -INFINITY ? 0.f : ex2_approx(m - top);
+        m = top;
+        l *= a;
+        acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+    };
+    for (int i0 = warp; i0 < n_part; i0 += 4 * kWarps) {
+        float2 ml[4];
+        float4 o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * kWarps;
+            const size_t si = (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * 8 * NT + row;
+            ml[j] = i < n_part ? P.part_ml[si] : make_float2(-INFINITY, 0.f);
+            o[j] = i < n_part ? reinterpret_cast<const float4 *>(P.part_o)[si * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const float top = fmaxf(fmaxf(m, ml[0].x), fmaxf(ml[1].x, fmaxf(ml[2].x, ml[3].x)));
+        if (top > m) raise(top);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) add(ml[j].x == -INFINITY ? 0.f : ex2_approx(ml[j].x - m), ml[j].y, o[j]);
     }
     so[warp][lane] = acc;
-    if (lane == 0) sl[warp] = l;
+    if (lane == 0) sml[warp] = make_float2(m, l);
     __syncthreads();
     if (warp != 0) return;
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) {
-        const float4 o = so[w][lane];
-        acc.x += o.x;
-        acc.y += o.y;
-        acc.z += o.z;
-        acc.w += o.w;
-        l += sl[w];
+        const float2 ml = sml[w];
+        if (ml.x > m) raise(ml.x);
+        add(ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m), ml.y, so[w][lane]);
     }
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
     const int tok = tok0 + x / P.group, hh = h * P.group + x % P.group;
