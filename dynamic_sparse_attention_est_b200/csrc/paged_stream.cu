@@ -64,7 +64,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return r;
 }
 // The pages a warp walks: 32 (logical block, page) entries at a time, one per
-// lane, the next 32 already loaded.
+// lane, the next 32 loaded ahead (once the first loads of keys are out: each entry
+// takes two or three dependent reads).
 template <bool kSparse>
 struct PageWalk {
     const PagedSeqs *S;
@@ -77,9 +78,10 @@ struct PageWalk {
         b = p = -1;
         if (slot >= n_slots) return;
         if (kSparse) {
+            const int before = __ldg(list + max(slot - 1, 0));
             b = __ldg(list + slot);
             // an entry that is negative, past the query's own page or not above the one before it is left out
-            if (b < 0 || b > last_blk || (slot > 0 && b <= __ldg(list + slot - 1))) {
+            if (b < 0 || b > last_blk || (slot > 0 && b <= before)) {
                 b = -1;
                 return;
             }
@@ -91,15 +93,16 @@ struct PageWalk {
     __device__ __forceinline__ void start(int slot, int lane) {
         base = slot;
         fetch(base + lane, blk, pg);
-        fetch(base + 32 + lane, blk_next, pg_next);
+        blk_next = pg_next = -1;
     }
+    __device__ __forceinline__ void ahead(int lane) { fetch(base + 32 + lane, blk_next, pg_next); }
     // Entry `slot`, not before the one asked for last; the whole warp calls it.
     __device__ __forceinline__ void get(int slot, int lane, int &b, int &p) {
         while (slot >= base + 32) {
             base += 32;
             blk = blk_next;
             pg = pg_next;
-            fetch(base + 32 + lane, blk_next, pg_next);
+            ahead(lane);
         }
         b = __shfl_sync(0xffffffffu, blk, slot - base);
         p = __shfl_sync(0xffffffffu, pg, slot - base);
@@ -252,7 +255,7 @@ __device__ __forceinline__ void run_piece(const StreamParams &SP, const Item &it
     walk.list = list;
     walk.seq = it.seq;
     walk.last_blk = kSparse ? it.pos0 >> S.page_log2 : 0;
-    walk.n_slots = kSparse ? n_list : (it.len + S.page - 1) >> S.page_log2;
+    walk.n_slots = min(kSparse ? n_list : (it.len + S.page - 1) >> S.page_log2, ((g1 - 1) >> gp_log2) + 1);
     walk.start((g0 + warp) >> gp_log2, lane);
 
     int stage_key = -1;  // lane s: first key of the group in stage s, -1 if none
@@ -280,6 +283,7 @@ __device__ __forceinline__ void run_piece(const StreamParams &SP, const Item &it
     if (ok)
 #pragma unroll
         for (int st = 0; st < kStages; ++st) fill(st, g0 + warp + st * kWarps);
+    walk.ahead(lane);
 
     // query fragments: row r of each 8-row tile, channels 16 kk + 2 c, + 1, + 8, + 9
     uint32_t qf[NT][8][2];
