@@ -63,6 +63,44 @@ __device__ __forceinline__ int page_of(const PagedSeqs &S, int s, int b, WsHeade
     return p;
 }
 
+// Item `idx` of a call in which sequence s has count(s) items: its sequence and which
+// of that one's items it is.  The whole CTA calls it; false if there are fewer items.
+template <int kThreads, class Count>
+__device__ __forceinline__ bool find_item(int n_seqs, int idx, Count count, int &seq, int &item) {
+    __shared__ int sums[kThreads / 32], hit[2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = (n_seqs + kThreads - 1) / kThreads;
+    const int sa = min((int)threadIdx.x * per, n_seqs), sb = min(sa + per, n_seqs);
+    int mine = 0;
+    for (int s = sa; s < sb; ++s) mine += count(s);
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) sums[warp] = inc;
+    if (threadIdx.x == 0) hit[0] = -1;
+    __syncthreads();
+    int at = inc - mine;
+    for (int w = 0; w < warp; ++w) at += sums[w];
+    if (at <= idx && idx < at + mine) {
+        for (int s = sa;; ++s) {
+            const int n = count(s);
+            if (idx < at + n) {
+                hit[0] = s;
+                hit[1] = idx - at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    seq = hit[0];
+    item = hit[1];
+    return seq >= 0;
+}
+
 // 16-bit float pairs of the two cache types.
 struct Bf16 {
     using T = __nv_bfloat16;
@@ -203,6 +241,7 @@ struct AppendParams {
     long long k_ts, k_hs, v_ts, v_hs, q_ts, q_hs, qo_ts, qo_hs;  // token and head strides, in elements
     long long kc_ps, vc_ps;                                      // page strides of the caches
     int hq, hkv, rot, rope_rows;
+    bool packed;  // grid x counts the pages of all sequences, not those of one
     WsHeader *hdr;
 };
 cudaError_t run_paged_append(const AppendParams &P, bool fp16, bool interleaved, cudaStream_t st);
@@ -252,7 +291,8 @@ struct EstimateParams {
     int hq, hkv, group, topk;
     int *blk_idx, *blk_cnt;  // [total][hkv][topk], [total][hkv]
     float *scores;           // [batch][hkv][score_stride]
-    float *top;              // [n_seqs * tiles][hkv][ranges] largest |bound| of a tile's page range
+    float *top;              // [batch][hkv][ranges] at a tile's first token: largest |bound| of its page range
+    bool packed;             // grid x counts the tiles of all sequences, not those of one
     int score_stride, batch;
     int t0, t1, tiles, tile_tokens, pages_per_cta, ranges;  // per launch
     WsHeader *hdr;
@@ -262,7 +302,7 @@ struct EstimatePlan {
     int score_stride, batch;  // batch: tokens scored at a time
     size_t n_scores, n_top;
 };
-EstimatePlan paged_estimate_plan(int total, int n_seqs, int max_q, int hkv, int width);
+EstimatePlan paged_estimate_plan(int total, int n_seqs, int hkv, int width);
 cudaError_t run_paged_estimate(const EstimateParams &P, bool fp16, cudaStream_t st);
 
 }  // namespace minf

@@ -226,7 +226,7 @@ size_t minf_paged_workspace_bytes(int op, int hq, int hkv, int total, int n_seqs
         return dense_sizes(n_seqs, hq / hkv, max_q).total;
     case MINF_OP_PAGED_BLOCK_ESTIMATE:
         if (topk < 1 || width < 1 || width > kMaxBlocks) return 0;
-        return estimate_bytes(paged_estimate_plan(total, n_seqs, max_q, hkv, width), nullptr);
+        return estimate_bytes(paged_estimate_plan(total, n_seqs, hkv, width), nullptr);
     case MINF_OP_PAGED_BLOCK_ATTENTION:
         if (topk < 1) return 0;
         return sparse_sizes(total, hkv, hq / hkv, topk, 128).total;  // the largest pages make the most shares
@@ -330,7 +330,7 @@ int minf_paged_block_estimate(const minf_paged_seqs *seqs, int dtype, int hq, in
     if ((rc = check_rows(q, "q", S.total, hq, false))) return rc;
     if (!k_bounds || !aligned16(k_bounds)) return bad(MINF_ERR_INVALID, "null or unaligned k_bounds");
     if (!blk_idx || !blk_cnt) return bad(MINF_ERR_INVALID, "null blk_idx or blk_cnt");
-    const EstimatePlan p = paged_estimate_plan(S.total, S.n_seqs, S.max_q, hkv, S.width);
+    const EstimatePlan p = paged_estimate_plan(S.total, S.n_seqs, hkv, S.width);
     size_t top_at = 0;
     if ((rc = api_check_ws(ws, ws_bytes, estimate_bytes(p, &top_at)))) return rc;
     P.q = q->data;

@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(ScoreShape::kThreads, 2) paged_scores_kernel(c
         if (threadIdx.x == 0) {
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, warp_top[w]);
-            P.top[((long long)blockIdx.x * P.hkv + h) * gridDim.z + blockIdx.z] = fmaxf(top, 0.f);
+            P.top[((long long)(ta - P.t0) * P.hkv + h) * P.ranges + blockIdx.z] = fmaxf(top, 0.f);
         }
     }
 }
@@ -291,9 +291,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_scores_tc_kernel(const __
     float *warp_top = reinterpret_cast<float *>(bar + 3);  // [8]
     const PagedSeqs &S = P.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.x / P.tiles, h = blockIdx.y;
+    const int h = blockIdx.y;
+    int s = blockIdx.x / P.tiles, tile = blockIdx.x % P.tiles;
+    if (P.packed) {
+        auto tiles = [&](int x) -> int {
+            const SeqView w = seq_view(S, x, P.hdr);
+            return (max(0, min(w.q0 + w.n, P.t1) - max(w.q0, P.t0)) + kTokLarge - 1) / kTokLarge;
+        };
+        if (!find_item<kTcThreads>(S.n_seqs, blockIdx.x, tiles, s, tile)) return;
+    }
     const SeqView v = seq_view(S, s, P.hdr);
-    const int ta = max(v.q0, P.t0) + (int)(blockIdx.x % P.tiles) * kTokLarge;
+    const int ta = max(v.q0, P.t0) + tile * kTokLarge;
     const int tb = min(min(v.q0 + v.n, P.t1), ta + kTokLarge);
     if (ta >= tb) return;
     const int last_pos = v.len - v.n + (tb - 1 - v.q0);
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_scores_tc_kernel(const __
         if (threadIdx.x == 0) {
 #pragma unroll
             for (int w = 0; w < kTcThreads / 32; ++w) top = fmaxf(top, warp_top[w]);
-            P.top[((long long)blockIdx.x * P.hkv + h) * gridDim.z + blockIdx.z] = fmaxf(top, 0.f);
+            P.top[((long long)(ta - P.t0) * P.hkv + h) * P.ranges + blockIdx.z] = fmaxf(top, 0.f);
         }
         if (warp == 0) tmem_dealloc(*tmem_slot, 128);
     }
@@ -498,7 +506,7 @@ constexpr int kWarpBorder = 128;
 // One (token, kv-head) row: where its candidates, scores and lists lie.
 struct Row {
     int s, tok, h, n, take;  // n candidate pages, take of them wanted; page n is the token's own
-    int tile_range0;         // first entry of its tile's page ranges in EstimateParams::top
+    long long tile_range0;   // first entry of its tile's page ranges in EstimateParams::top
     const float *sc;
     int *out;
 };
@@ -533,8 +541,8 @@ __device__ __forceinline__ bool row_setup(const EstimateParams &P, int row_in, i
         return false;
     }
     if (w.take == 0) return false;
-    const int tile = s * P.tiles + (w.tok - max(v.q0, P.t0)) / P.tile_tokens;
-    w.tile_range0 = (tile * P.hkv + w.h) * P.ranges;
+    const int t_first = max(v.q0, P.t0), tile = t_first + (w.tok - t_first) / P.tile_tokens * P.tile_tokens;
+    w.tile_range0 = ((long long)(tile - P.t0) * P.hkv + w.h) * P.ranges;
     w.sc = P.scores + (row - (long long)P.t0 * P.hkv) * P.score_stride;
     return true;
 }
@@ -1035,15 +1043,20 @@ cudaError_t launch_scores(EstimateParams &P, bool small, cudaStream_t st) {
         small ? allow_smem(reinterpret_cast<const void *>(paged_scores_kernel<Ty>), (int)ScoreShape::kBytes, done_small)
               : allow_smem(reinterpret_cast<const void *>(paged_scores_tc_kernel<Ty>), (int)kTcBytes, done_tc);
     if (e != cudaSuccess) return e;
-    // page ranges: one wave of CTAs over all (sequence, tile, kv-head)s
-    const long long rows = (long long)S.n_seqs * P.tiles * P.hkv;
+    // Tiles of the longest sequence for every one, or, where that is far above what all
+    // tokens can fill (a chunk beside many single tokens), that bound, each CTA finding
+    // its tile.
+    const long long by_seq = (long long)S.n_seqs * P.tiles, all = (P.t1 - P.t0) / kTokLarge + S.n_seqs;
+    P.packed = !small && by_seq > 2 * all;
+    const long long x = P.packed ? all : by_seq;
+    // page ranges: one wave of CTAs over all of them
     const int step = small ? ScoreShape::kWarps * kStepPages : kPageTile;
     const int pages = std::max(1, S.width - 1);  // candidates: the token's own page is none
     const int most = (pages + step - 1) / step;
-    const int z = (int)std::max<long long>(1, std::min<long long>({most, (small ? 296 : 148) / rows, kMaxRanges}));
+    const int z = (int)std::max<long long>(1, std::min<long long>({most, (small ? 296 : 148) / (x * P.hkv), kMaxRanges}));
     P.pages_per_cta = (most + z - 1) / z * step;
     P.ranges = (pages + P.pages_per_cta - 1) / P.pages_per_cta;
-    const dim3 grid((unsigned)(S.n_seqs * P.tiles), P.hkv, P.ranges);
+    const dim3 grid((unsigned)x, P.hkv, P.ranges);
     if (small) paged_scores_kernel<Ty><<<grid, ScoreShape::kThreads, ScoreShape::kBytes, st>>>(P);
     else paged_scores_tc_kernel<Ty><<<grid, kTcThreads, kTcBytes, st>>>(P);
     return cudaGetLastError();
@@ -1092,20 +1105,17 @@ cudaError_t launch(EstimateParams P, cudaStream_t st) {
 
 }  // namespace
 
-EstimatePlan paged_estimate_plan(int total, int n_seqs, int max_q, int hkv, int width) {
+EstimatePlan paged_estimate_plan(int total, int n_seqs, int hkv, int width) {
     EstimatePlan p{};
     p.score_stride = (width + 3) & ~3;
     // 64 MiB of scores at a time: written and read back inside L2
     const long long row = (long long)p.score_stride * 4 * hkv;
     p.batch = (int)std::max<long long>(1, std::min<long long>(total, (64ll << 20) / row));
     p.n_scores = (size_t)p.batch * hkv * p.score_stride;
-    // tiles of a launch: at most these (the last batch is no longer than the others, but
-    // may fall into the small tiles), times their ranges
-    const long long most = std::min(max_q, p.batch);
-    const long long tiles = std::max<long long>((most + kTokLarge - 1) / kTokLarge,
-                                                std::min<long long>(most, kTokSmall) > 0 ? 1 : 0);
-    const long long rows = (long long)n_seqs * tiles * hkv;
-    p.n_top = (size_t)std::max<long long>(rows, std::min<long long>(rows * kMaxRanges, 296));
+    // the ranges of a launch: see launch_scores
+    const long long most = (std::max(1, width - 1) + ScoreShape::kWarps * kStepPages - 1) / (ScoreShape::kWarps * kStepPages);
+    const long long ranges = std::max<long long>(1, std::min<long long>({most, 296 / ((long long)n_seqs * hkv), kMaxRanges}));
+    p.n_top = (size_t)(p.batch * hkv * ranges);
     return p;
 }
 

@@ -267,3 +267,42 @@ def test_block_estimate_many_rows_and_long_rows():
         idx, cnt = minf.minf_paged_block_estimate(c.q, kb, *c.meta(), page_size=page, topk=33)
         wi, wc = ref.estimate(c, kb, 33)
         assert torch.equal(cnt, wc) and torch.equal(idx, wi)
+
+
+def test_append_and_estimate_of_a_chunk_beside_many_single_tokens():
+    """The longest sequence far above the others: pages and tiles are found by what all tokens touch."""
+    lens = [1] * 40 + [0, 500] + [1] * 30 + [3, 700, 0]
+    kv = [1 + (i * 37) % 200 for i in range(len(lens))]
+    kv = [max(n, x) + (i % 5) for i, (n, x) in enumerate(zip(lens, kv))]
+    c = ref.Case(lens, kv, 4, 2, 16, BF, seed=21, extra_rows=3)
+    kb0 = torch.nan_to_num(ref.bounds(c))
+    idx, cnt = minf.minf_paged_block_estimate(c.q, kb0, *c.meta(), page_size=16, topk=6)
+    wi, wc = ref.estimate(c, kb0, 6)
+    n = sum(lens)
+    assert torch.equal(cnt[:n], wc[:n]) and torch.equal(idx[:n], wi[:n])
+    tab = rope_table(max(kv), 128)
+    kc, vc = torch.zeros_like(c.k_cache), torch.zeros_like(c.v_cache)
+    kb = torch.zeros(c.num_pages, 2, 2, 128, dtype=BF, device="cuda")
+    ws = minf.workspace(256, c.dev)
+    q = minf.minf_paged_append(c.k_new, c.v_new, kc, vc, *c.meta(), rope=tab, q=c.q, k_bounds=kb, ws=ws)
+    assert minf.minf_status(ws) == 0
+    rows = list(c.rows())
+    pos = torch.tensor([p for _, _, p in rows], device="cuda")
+    yk, tk = ref.rotate(c.k_new[:n], tab, pos, 128, False)
+    yq, tq = ref.rotate(c.q[:n], tab, pos, 128, False)
+    assert ((q[:n].double() - yq).abs() <= tq).all()
+    seq = torch.tensor([s for s, _, _ in rows], device="cuda")
+    page = c.tables[seq, pos // 16].long()
+    assert ((kc[page, :, pos % 16].double() - yk).abs() <= tk).all()
+    assert torch.equal(vc[page, :, pos % 16], c.v_new[:n])
+    written = torch.zeros(c.num_pages, 16, dtype=torch.bool, device="cuda")
+    written[page, pos % 16] = True
+    assert not kc.transpose(1, 2)[~written].any() and not vc.transpose(1, 2)[~written].any()
+    for s, (m, x) in enumerate(zip(lens, kv)):
+        for b in range((x - m) // 16, (x - 1) // 16 + 1 if m else 0):
+            pg, a = int(c.tables[s, b]), max(0, x - m - 16 * b)
+            keys = kc[pg, :, a:min(16, x - 16 * b)]
+            lo, hi = keys.amin(1), keys.amax(1)
+            if a:  # joined with what stood there: zeros
+                lo, hi = lo.clamp(max=0), hi.clamp(min=0)
+            assert torch.equal(kb[pg, :, 0], lo) and torch.equal(kb[pg, :, 1], hi)
