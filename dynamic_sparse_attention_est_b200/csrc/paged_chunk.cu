@@ -80,6 +80,16 @@ __device__ __forceinline__ void umma_ts_half_warp(uint32_t d, uint32_t a_tmem, u
         : "memory");
 }
 
+// The MMA warps' wait: P is a few hundred clocks away most of the time, and two
+// spinning warps leave the SM's issue slots alone (2 % of the kernel's time; spinning
+// softmax warps, eight of them, cost 16 %).  Bounded like the others in the end.
+__device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity, const WaitCtl &w, int site) {
+#pragma unroll 1
+    for (int i = 0; i < 100000; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return wait_bounded(bar, parity, w, site);
+}
+
 struct ChunkParams {
     CUtensorMap tmap_q;  // {128, G, total, hkv}, box {64, G, tokens per tile, 1}
     CUtensorMap tmap_k;  // {128, P, hkv, pages}, box {64, min(P, 64), 1, 1}
@@ -383,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             uint32_t pp = 0;         // parity of the next P of each half
             bool ok = true;
             auto wait_full = [&](int f, int site) -> bool {
-                return __all_sync(0xffffffffu, wait_bounded_sleep(bar(B_FULL + f % kStages), (f / kStages) & 1, wc, site));
+                return __all_sync(0xffffffffu, wait_spin(bar(B_FULL + f % kStages), (f / kStages) & 1, wc, site));
             };
             auto issue_s = [&](int h, int f) {
                 umma_ss_tile_warp(tmem + t * 128 + h * 64, dq + (uint64_t)((t * kTileBytes) >> 4),
@@ -396,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 if (t == 1 && !n.two) {
                     // Nothing to multiply, but every stage is taken and given back: a warp that
                     // ran ahead of the ring would take an older phase's parity for its own.
-                    ok = __all_sync(0xffffffffu, wait_bounded_sleep(bar(B_Q_FULL), n_q & 1, wc, wait_site(3, B_Q_FULL, u)));
+                    ok = __all_sync(0xffffffffu, wait_spin(bar(B_Q_FULL), n_q & 1, wc, wait_site(3, B_Q_FULL, u)));
                     if (!ok) break;
                     ++n_q;
                     if (lane == 0) mbar_arrive(bar(B_Q_EMPTY));
@@ -406,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     }
                     continue;
                 }
-                ok = __all_sync(0xffffffffu, wait_bounded_sleep(bar(B_Q_FULL), n_q & 1, wc, wait_site(3, B_Q_FULL, u)));
+                ok = __all_sync(0xffffffffu, wait_spin(bar(B_Q_FULL), n_q & 1, wc, wait_site(3, B_Q_FULL, u)));
                 if (!ok || !(ok = wait_full(used, wait_site(3, B_FULL, 0)))) break;
                 ++n_q;
                 tc_fence_after();
@@ -422,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int b = 2 * t + h;
-                        ok = __all_sync(0xffffffffu, wait_bounded_sleep(bar(B_P_FULL + b), (pp >> h) & 1, wc,
+                        ok = __all_sync(0xffffffffu, wait_spin(bar(B_P_FULL + b), (pp >> h) & 1, wc,
                                                                   wait_site(3, B_P_FULL + b, j)));
                         if (!ok) break;
                         pp ^= 1u << h;
@@ -641,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 // One CTA per 32 rows of a cut pair at a time, one warp per row: its parts in order.
 constexpr int kJoinRows = 32;
 template <class Ty>
-__global__ void __launch_bounds__(256, 5) paged_chunk_join_kernel(const __grid_constant__ PagedAttnParams P, int tpt,
+__global__ void __launch_bounds__(256, 4) paged_chunk_join_kernel(const __grid_constant__ PagedAttnParams P, int tpt,
                                                                int part_rows) {
     const PagedSeqs &S = P.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -662,27 +672,37 @@ __global__ void __launch_bounds__(256, 5) paged_chunk_join_kernel(const __grid_c
         const int pairs = seq_pairs(v, tpt), parts = seq_parts(seq_ktiles(v), part_len);
         const int rem = item - pre[lo].y, h = rem / pairs, at = rem % pairs;
         const size_t slot0 = (size_t)pre[lo].x + (size_t)h * parts * pairs + at;  // part i: pairs further on
+#pragma unroll 2
         for (int x = warp; x < kJoinRows; x += 8) {
             const int r = (w % per) * kJoinRows + x, in = (r & 127) / P.group;
             const int tok = ((pairs - 1 - at) * 2 + (r >> 7)) * tpt + in;
             if (in >= tpt || tok >= v.n) continue;
-            float m = -INFINITY;
-            for (int i = lane; i < parts; i += 32) m = fmaxf(m, P.part_ml[(slot0 + (size_t)i * pairs) * part_rows + r].x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            float l = 0.f;
+            float m = -INFINITY, l = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int i = 0; i < parts; ++i) {
-                const size_t row = (slot0 + (size_t)i * pairs) * part_rows + r;
-                const float2 ml = P.part_ml[row];
-                const float4 o = reinterpret_cast<const float4 *>(P.part_o)[row * 32 + lane];
-                const float a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-                l = fmaf(ml.y, a, l);
-                acc.x = fmaf(o.x, a, acc.x);
-                acc.y = fmaf(o.y, a, acc.y);
-                acc.z = fmaf(o.z, a, acc.z);
-                acc.w = fmaf(o.w, a, acc.w);
+            for (int i0 = 0; i0 < parts; i0 += 4) {  // four parts in flight
+                float2 ml[4];
+                float4 o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const size_t row = (slot0 + (size_t)(i0 + j) * pairs) * part_rows + r;
+                    ml[j] = i0 + j < parts ? P.part_ml[row] : make_float2(-INFINITY, 0.f);
+                    o[j] = i0 + j < parts ? reinterpret_cast<const float4 *>(P.part_o)[row * 32 + lane]
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                const float top = fmaxf(fmaxf(m, ml[0].x), fmaxf(ml[1].x, fmaxf(ml[2].x, ml[3].x)));
+                const float a0 = m == -INFINITY ? 0.f : ex2_approx(m - top);
+                m = top;
+                l *= a0;
+                acc = make_float4(acc.x * a0, acc.y * a0, acc.z * a0, acc.w * a0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float a = ml[j].x == -INFINITY ? 0.f : ex2_approx(ml[j].x - m);
+                    l = fmaf(ml[j].y, a, l);
+                    acc.x = fmaf(o[j].x, a, acc.x);
+                    acc.y = fmaf(o[j].y, a, acc.y);
+                    acc.z = fmaf(o[j].z, a, acc.z);
+                    acc.w = fmaf(o[j].w, a, acc.w);
+                }
             }
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
             const int hh = h * P.group + (r & 127) % P.group;
