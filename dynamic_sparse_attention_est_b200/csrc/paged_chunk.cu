@@ -106,42 +106,77 @@ __device__ __forceinline__ int seq_ktiles(const SeqView &v) { return (v.len + kK
 __device__ __forceinline__ int seq_parts(int ktiles, int part_len) {
     return max(1, (ktiles + part_len - 1) / part_len);
 }
+// A plan: the part length, and whether whole rounds of pairs stay uncut (part_len < 0
+// in the encoded form), which a call with one sequence to work on may choose.
+struct PartPlan {
+    int len;
+    bool tail;
+};
+__device__ __forceinline__ PartPlan part_plan(int code) { return {abs(code), code < 0}; }
+// How a sequence's pairs (over its kv-heads) are cut: the first `whole` are units of
+// their own, the others are cut into `parts` each.
+struct SeqCut {
+    int items, whole, parts;
+    __device__ int units() const { return whole + (items - whole) * parts; }
+    __device__ int slots() const { return parts > 1 ? (items - whole) * parts : 0; }
+};
+__device__ __forceinline__ SeqCut seq_cut(const SeqView &v, int hkv, int tpt, const PartPlan &p) {
+    SeqCut c;
+    c.items = hkv * seq_pairs(v, tpt);
+    c.parts = seq_parts(seq_ktiles(v), p.len);
+    c.whole = c.parts > 1 && p.tail ? c.items / kGrid * kGrid : 0;
+    return c;
+}
 
 // Chooses the part length: candidate i cuts the longest sequence into i + 1 parts.
 // The estimated time of a candidate is that of its rounds of units (kGrid at a
 // time) of average length, a tail of one longest unit, and per unit two tiles'
 // time for its prologue and epilogue, four more for the traffic of its partial
 // result (256 KB written and read); candidates whose cut units exceed the
-// partial slots are out.  Every CTA computes the same result.
+// partial slots are out.  If a single sequence has new tokens (a chunk of a long
+// prompt), its whole rounds of pairs may stay uncut and the rest alone be cut: 256
+// pairs of 448 tiles take 1,637 us cut into 4 each, 1,578 us with the last 108 cut.  Every
+// CTA computes the same result.
 struct PlanSum {
     long long units, cut;
     float work;
+    int kt, seqs;
 };
 __device__ int choose_part_len(const ChunkParams &P, PlanSum (*sum)[32], int *len_sh) {
     const PagedSeqs &S = P.a.seqs;
     constexpr int kWarps = kThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int kt_max = 1;
+    int kt_max = 1, seqs = 0;
     for (int s = threadIdx.x; s < S.n_seqs; s += kThreads) {
         const SeqView v = seq_view(S, s, P.a.hdr);
-        if (v.n > 0) kt_max = max(kt_max, seq_ktiles(v));
+        if (v.n > 0) {
+            kt_max = max(kt_max, seq_ktiles(v));
+            ++seqs;
+        }
     }
     kt_max = __reduce_max_sync(0xffffffffu, kt_max);
-    if (lane == 0) sum[warp][0].units = kt_max;
+    seqs = __reduce_add_sync(0xffffffffu, seqs);
+    if (lane == 0) {
+        sum[warp][0].kt = kt_max;
+        sum[warp][0].seqs = seqs;
+    }
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) kt_max = max(kt_max, (int)sum[w][0].units);
+    seqs = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        kt_max = max(kt_max, sum[w][0].kt);
+        seqs += sum[w][0].seqs;
+    }
     __syncthreads();
     // lane = candidate, each warp its share of the sequences
     const int len = (kt_max + lane) / (lane + 1);
-    PlanSum mine{0, 0, 0.f};
+    PlanSum mine{0, 0, 0.f, 0, 0};
     for (int s = warp; s < S.n_seqs; s += kWarps) {
         const SeqView v = seq_view(S, s, P.a.hdr);
         if (v.n == 0) continue;
-        const int kt = seq_ktiles(v), parts = seq_parts(kt, len);
-        const long long items = (long long)P.a.hkv * seq_pairs(v, P.tpt);
-        mine.units += items * parts;
-        if (parts > 1) mine.cut += items * parts;
-        mine.work += (float)items * (float)kt;
+        const SeqCut c = seq_cut(v, P.a.hkv, P.tpt, {len, false});
+        mine.units += c.units();
+        mine.cut += c.slots();
+        mine.work += (float)c.items * (float)seq_ktiles(v);
     }
     sum[warp][lane] = mine;
     __syncthreads();
@@ -151,17 +186,31 @@ __device__ int choose_part_len(const ChunkParams &P, PlanSum (*sum)[32], int *le
             mine.cut += sum[w][lane].cut;
             mine.work += sum[w][lane].work;
         }
+        constexpr float kOwn = 2.f, kCut = 6.f;  // tiles' time that a unit, a cut unit costs besides its tiles
         float cost = INFINITY;
+        int code = len;
         if (mine.cut <= P.max_slots && mine.units > 0) {
             const float avg = mine.work / (float)mine.units;
             const float rounds = (float)((mine.units + kGrid - 1) / kGrid);
-            cost = rounds * (avg + (mine.cut > 0 ? 6.f : 2.f)) + fmaxf(0.f, (float)len - avg);
+            cost = rounds * (avg + (mine.cut > 0 ? kCut : kOwn)) + fmaxf(0.f, (float)len - avg);
+        }
+        if (seqs == 1 && lane > 0 && mine.units > 0) {
+            const int parts = seq_parts(kt_max, len);
+            const long long items = mine.units / parts, rest = items % kGrid;
+            if (rest > 0 && rest * parts <= P.max_slots) {
+                const float c = (float)(items / kGrid) * ((float)kt_max + kOwn) +
+                                (float)((rest * parts + kGrid - 1) / kGrid) * ((float)kt_max / (float)parts + kCut);
+                if (c < cost) {
+                    cost = c;
+                    code = -len;
+                }
+            }
         }
         float best = cost;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
         const unsigned at = __ballot_sync(0xffffffffu, cost <= best);
-        if (lane == __ffs(at) - 1) *len_sh = max(1, len);
+        if (lane == __ffs(at) - 1) *len_sh = code;
     }
     __syncthreads();
     return *len_sh;
@@ -176,7 +225,7 @@ struct Unit {
     bool two;          // the second row tile holds tokens
 };
 
-__device__ __forceinline__ Unit unit_at(const ChunkParams &P, const int2 *pre, int part_len, int u) {
+__device__ __forceinline__ Unit unit_at(const ChunkParams &P, const int2 *pre, const PartPlan &plan, int u) {
     const PagedSeqs &S = P.a.seqs;
     int lo = 0, hi = S.n_seqs;
     while (hi - lo > 1) {
@@ -188,12 +237,21 @@ __device__ __forceinline__ Unit unit_at(const ChunkParams &P, const int2 *pre, i
     Unit n;
     n.s = lo;
     const SeqView v = seq_view(S, lo, P.a.hdr);
-    const int pairs = seq_pairs(v, P.tpt);
-    n.parts = seq_parts(seq_ktiles(v), part_len);
-    const int rem = u - pre[lo].x;
-    n.pair = pairs - 1 - rem % pairs;  // the longest first
-    n.part = (rem / pairs) % n.parts;
-    n.h = rem / pairs / n.parts;
+    const int pairs = seq_pairs(v, P.tpt), rem = u - pre[lo].x;
+    const SeqCut c = seq_cut(v, P.a.hkv, P.tpt, plan);
+    int item = rem;
+    n.part = 0;
+    n.parts = 1;
+    n.slot = -1;
+    if (rem >= c.whole && c.parts > 1) {
+        const int cut = c.items - c.whole;
+        n.parts = c.parts;
+        n.part = (rem - c.whole) / cut;  // a part of every pair before the next
+        item = c.whole + (rem - c.whole) % cut;
+        n.slot = pre[lo].y + rem - c.whole;
+    }
+    n.h = item / pairs;
+    n.pair = pairs - 1 - item % pairs;  // the longest first
     n.tok0 = n.pair * 2 * P.tpt;
     n.n_tok = min(2 * P.tpt, v.n - n.tok0);
     n.two = n.n_tok > P.tpt;
@@ -204,7 +262,6 @@ __device__ __forceinline__ Unit unit_at(const ChunkParams &P, const int2 *pre, i
     const int kt = last < 0 ? 0 : last / kKeyTile + 1;
     n.ka = (int)((long long)kt * n.part / n.parts);
     n.kb = (int)((long long)kt * (n.part + 1) / n.parts);
-    n.slot = n.parts > 1 ? pre[lo].y + rem : -1;
     return n;
 }
 
@@ -250,17 +307,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         tmem_relinquish();
     }
     // ---- plan: part length, then per sequence the units and partial slots before it
-    const int part_len =
+    const int code =
         choose_part_len(P, reinterpret_cast<PlanSum(*)[32]>(smem + kSmemRing), len_sh);  // the ring is not in use yet
+    const PartPlan plan = part_plan(code);
     {
         const int per = (S.n_seqs + kThreads - 1) / kThreads;
         const int sa = min((int)threadIdx.x * per, S.n_seqs), sb = min(sa + per, S.n_seqs);
         auto count = [&](int s) -> int2 {
             const SeqView v = seq_view(S, s, P.a.hdr);
             if (v.n == 0) return make_int2(0, 0);
-            const int parts = seq_parts(seq_ktiles(v), part_len);
-            const int u = P.a.hkv * seq_pairs(v, P.tpt) * parts;
-            return make_int2(u, parts > 1 ? u : 0);
+            const SeqCut c = seq_cut(v, P.a.hkv, P.tpt, plan);
+            return make_int2(c.units(), c.slots());
         };
         int2 mine = make_int2(0, 0);
         for (int s = sa; s < sb; ++s) {
@@ -305,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             int mine = 0;
             if (s < S.n_seqs && pre[s + 1].y > pre[s].y) {
                 const SeqView v = seq_view(S, s, P.a.hdr);
-                mine = P.a.hkv * seq_pairs(v, P.tpt);
+                const SeqCut c = seq_cut(v, P.a.hkv, P.tpt, plan);
+                mine = c.items - c.whole;
             }
             int inc = mine;
 #pragma unroll
@@ -316,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             if (s <= S.n_seqs) dst[s] = make_int2(pre[s].y, cut + inc - mine);
             cut += __shfl_sync(0xffffffffu, inc, 31);
         }
-        if (lane == 0) P.a.plan[0] = part_len;
+        if (lane == 0) P.a.plan[0] = code;
     }
     const uint32_t tmem = *tmem_slot;
     const WaitCtl wc{abort_flag, &P.a.hdr->status, P.a.wait_limit_ns};
@@ -336,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 return max(0, page_of(S, n.s, key >> S.page_log2, P.a.hdr));  // a bad one is flagged, its keys are page 0's
             };
             for (int u = blockIdx.x; ok && u < n_units; u += gridDim.x) {
-                const Unit n = unit_at(P, pre, part_len, u);
+                const Unit n = unit_at(P, pre, plan, u);
                 if (n.ka >= n.kb) continue;
                 int pg = page_for(n, n.ka);
                 ok = __all_sync(0xffffffffu, wait_bounded_sleep(bar(B_Q_EMPTY), (n_q & 1) ^ 1, wc, wait_site(1, B_Q_EMPTY, u)));
@@ -400,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                                   dk + (uint64_t)(((f % kStages) * kTileBytes + h * 8192) >> 4), kQK, 0u);
             };
             for (int u = blockIdx.x; ok && u < n_units; u += gridDim.x) {
-                const Unit n = unit_at(P, pre, part_len, u);
+                const Unit n = unit_at(P, pre, plan, u);
                 const int T = n.kb - n.ka;
                 if (T <= 0) continue;
                 if (t == 1 && !n.two) {
@@ -489,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         uint32_t sp = 0, op = 0;  // parity of the next S of each half, and of the unit's O
         bool ok = true;
         for (int u = blockIdx.x; ok && u < n_units; u += gridDim.x) {
-            const Unit n = unit_at(P, pre, part_len, u);
+            const Unit n = unit_at(P, pre, plan, u);
             if (t == 1 && !n.two) continue;
             const int tok = n.tok0 + t * P.tpt + r / G;  // in the sequence
             const int n_here = min(P.tpt, n.n_tok - t * P.tpt);
@@ -656,7 +714,7 @@ __global__ void __launch_bounds__(256, 4) paged_chunk_join_kernel(const __grid_c
     const PagedSeqs &S = P.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     wait_for_primary();
-    const int part_len = (int)P.plan[0];
+    const PartPlan plan = part_plan((int)P.plan[0]);
     const int2 *pre = reinterpret_cast<const int2 *>(P.plan + 1);  // (slots, pairs) cut before each sequence
     const int n_pairs = pre[S.n_seqs].y;
     const int per = part_rows / kJoinRows;
@@ -669,9 +727,11 @@ __global__ void __launch_bounds__(256, 4) paged_chunk_join_kernel(const __grid_c
             else hi = mid;
         }
         const SeqView v = seq_view(S, lo, P.hdr);
-        const int pairs = seq_pairs(v, tpt), parts = seq_parts(seq_ktiles(v), part_len);
-        const int rem = item - pre[lo].y, h = rem / pairs, at = rem % pairs;
-        const size_t slot0 = (size_t)pre[lo].x + (size_t)h * parts * pairs + at;  // part i: pairs further on
+        const int pairs = seq_pairs(v, tpt), rem = item - pre[lo].y;
+        const SeqCut c = seq_cut(v, P.hkv, tpt, plan);
+        const int parts = c.parts, cut = c.items - c.whole;  // part i of a pair: i * cut slots further on
+        const int h = (c.whole + rem) / pairs, at = (c.whole + rem) % pairs;
+        const size_t slot0 = (size_t)pre[lo].x + (size_t)rem;
 #pragma unroll 2
         for (int x = warp; x < kJoinRows; x += 8) {
             const int r = (w % per) * kJoinRows + x, in = (r & 127) / P.group;
@@ -684,7 +744,7 @@ __global__ void __launch_bounds__(256, 4) paged_chunk_join_kernel(const __grid_c
                 float4 o[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const size_t row = (slot0 + (size_t)(i0 + j) * pairs) * part_rows + r;
+                    const size_t row = (slot0 + (size_t)(i0 + j) * cut) * part_rows + r;
                     ml[j] = i0 + j < parts ? P.part_ml[row] : make_float2(-INFINITY, 0.f);
                     o[j] = i0 + j < parts ? reinterpret_cast<const float4 *>(P.part_o)[row * 32 + lane]
                                           : make_float4(0.f, 0.f, 0.f, 0.f);

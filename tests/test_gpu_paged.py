@@ -306,3 +306,22 @@ def test_append_and_estimate_of_a_chunk_beside_many_single_tokens():
             if a:  # joined with what stood there: zeros
                 lo, hi = lo.clamp(max=0), hi.clamp(min=0)
             assert torch.equal(kb[pg, :, 0], lo) and torch.equal(kb[pg, :, 1], hi)
+
+
+def test_chunk_with_whole_rounds_uncut():
+    """One sequence whose row-tile pairs fill the SMs once and a third: the first round's pairs stay
+    whole, the rest are cut and joined."""
+    n, kv, hq, hkv = 1275, 3300, 40, 10
+    c = ref.Case([n, 0], [kv, 9], hq, hkv, 64, BF, seed=31)
+    out, lse = minf.minf_paged_attention(c.q, c.k_cache, c.v_cache, *c.meta(), scale=SCALE)
+    hide = torch.arange(kv, device="cuda") > torch.arange(kv - n, kv, device="cuda")[:, None]
+    for h in range(hq):
+        k, v = c.stored(0, h // 4, kv)
+        x = (c.q[:, h].double() @ k.T) * SCALE
+        d = 2 ** -19 * float((c.q[:, h].double().abs() @ k.abs().T).max()) * SCALE + 2 ** -19  # error of a logit
+        x.masked_fill_(hide, -math.inf)
+        z = torch.logsumexp(x, 1)
+        p = (x - z[:, None]).exp()
+        tol = ref.u(BF) * (p @ v).abs() + (ref.u(BF) + 2 * d) * (p @ v.abs()) + 1e-7
+        assert ((out[:, h].double() - p @ v).abs() <= tol).all(), h
+        assert ((lse[:, h].double() - z).abs() <= d + kv * 2 ** -24 + 1e-5).all(), h
