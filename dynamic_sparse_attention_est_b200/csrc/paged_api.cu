@@ -109,7 +109,10 @@ int check_cache(const minf_paged_cache *c, int hkv, int page) {
     return MINF_OK;
 }
 
-// Query rows (tokens x group) up to which a call takes the streaming kernel.
+// Query rows (tokens x group) up to which a call takes the streaming kernel: two of
+// its 8-row tiles, one read of K and V.  32 sequences of 8K tokens, four q-heads to a
+// kv-head: 16 rows 185 us streaming; 20 rows 196 us with the chunk kernel (which takes
+// as long for one row as for 128) and 338 us streaming, which reads K and V twice.
 constexpr int kStreamMaxRows = 16;
 bool streams(int max_q, int group) { return (long long)max_q * group <= kStreamMaxRows; }
 
