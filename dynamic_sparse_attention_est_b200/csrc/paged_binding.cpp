@@ -3,8 +3,8 @@
 // pointers and strides handed to the C ABI, outputs allocated by torch.
 //
 // A decoding step calls these once per layer on kernels of a few microseconds.
-// Reading a dozen tensors' attributes through Python takes 15 to 20 us a call; here
-// it takes one.
+// Host time of a call with the attributes read in Python and the C ABI reached by
+// ctypes: 27 us for the append, 30 us for attention; here 5 us and 10 to 16 us.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 

@@ -11,8 +11,10 @@
 // A row tile's S has two 64-key halves that are handed over separately: while the
 // softmax works on one half, the tensor cores multiply P of the other half by V
 // and write the S of 64 keys further on over it, so neither side waits for the
-// other's latency.  (With whole 128-key tiles in turn, S -> softmax -> P V -> S is
-// one chain per row tile: 4,440 clocks for 128 keys against 256 rows.)
+// other's latency.  With whole 128-key tiles S -> softmax -> P V -> S is one chain
+// per row tile: 2,048 tokens over 55,296 + 2,048 kept the SMs busy for 1,575 us, with
+// halves for 1,524 us (3,750 and 3,590 clocks for 128 keys against 256 rows; both
+// with one issuing warp a row tile).
 //
 // Warp roles (384 threads, one persistent CTA per SM):
 //   warp 0       TMA producer: Q of a unit, then K and V tiles in turn through one
