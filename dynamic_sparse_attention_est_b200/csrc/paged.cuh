@@ -193,6 +193,12 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
 // the first allows it with launch_dependents.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The end of a kernel launched that way.  Its CTAs may leave without needing the first
+// kernel's results, but the grid must not end before that kernel: what follows it in the
+// stream waits for this grid alone.  One CTA that waits holds the grid.
+__device__ __forceinline__ void end_after_primary() {
+    if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0) wait_for_primary();
+}
 
 // Lets `kernel` take `bytes` of dynamic shared memory on the current device; a
 // kernel's `done` remembers the devices on which that is set (a launch per layer

@@ -656,8 +656,7 @@ struct alignas(16) WarpShared {
 };
 
 template <class Ty, int kPer>
-__global__ void __launch_bounds__(kSelectThreads, kPer == 32 ? 3 : 2)
-    paged_select_warp_kernel(const __grid_constant__ EstimateParams P) {
+__device__ __forceinline__ void select_row_warp(const EstimateParams &P) {
     __shared__ WarpShared all[kSelectWarps];
     const int lane = threadIdx.x & 31;
     WarpShared &sh = all[threadIdx.x >> 5];
@@ -829,6 +828,13 @@ __global__ void __launch_bounds__(kSelectThreads, kPer == 32 ? 3 : 2)
     }
 }
 
+template <class Ty, int kPer>
+__global__ void __launch_bounds__(kSelectThreads, kPer == 32 ? 3 : 2)
+    paged_select_warp_kernel(const __grid_constant__ EstimateParams P) {
+    select_row_warp<Ty, kPer>(P);
+    end_after_primary();
+}
+
 // ---- one CTA per row, its keys in shared memory
 struct alignas(16) SelectShared {
     double q[2 * kD];  // Q- then Q+, read 16 bytes at a time
@@ -866,7 +872,7 @@ __device__ __forceinline__ unsigned block_prefix(unsigned x, unsigned &total, Se
 }
 
 template <class Ty>
-__global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __grid_constant__ EstimateParams P) {
+__device__ __forceinline__ void select_row(const EstimateParams &P) {
     extern __shared__ uint32_t keys[];  // [candidates]
     __shared__ SelectShared sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -1031,6 +1037,12 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
         if (yes && to < (unsigned)w.take) w.out[to] = i0 + lane;
         at += __popc(bal);
     }
+}
+
+template <class Ty>
+__global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __grid_constant__ EstimateParams P) {
+    select_row<Ty>(P);
+    end_after_primary();
 }
 
 constexpr int kMaxRanges = 64;  // page ranges of a score launch

@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 2)
 // kernel before cut them; all that needs no result of that kernel is done while it
 // still runs.
 template <class Ty, int NT, bool kSparse>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedAttnParams P) {
+__device__ __forceinline__ void join_row(const PagedAttnParams &P) {
     constexpr int kWarps = kJoinWarps, kThreads = 32 * kJoinWarps;
     __shared__ float4 so[kWarps][32];
     __shared__ float2 sml[kWarps];
@@ -730,6 +730,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
     *dst = make_uint2(Ty::pack(acc.x * inv, acc.y * inv), Ty::pack(acc.z * inv, acc.w * inv));
     if (lane == 0 && P.lse)
         P.lse[(size_t)tok * P.hq + hh] = l == 0.f ? -INFINITY : (m - Ty::kShift + __log2f(l)) * 0.69314718055994531f;
+}
+
+template <class Ty, int NT, bool kSparse>
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedAttnParams P) {
+    join_row<Ty, NT, kSparse>(P);
+    end_after_primary();
 }
 
 template <class Ty, int NT>
