@@ -24,6 +24,8 @@ constexpr int kMaxSeqs = 4096;  // sequences per call (their prefix sums sit in 
 enum : int { BAD_SEQ = 1, BAD_PAGE = 2, BAD_POSITION = 3, BAD_BLOCK = 4 };
 
 __device__ __forceinline__ void flag_invalid(WsHeader *hdr, int what) {
+    // every CTA may find the same fault thousands of times: only the first ones write
+    if (*reinterpret_cast<volatile int *>(&hdr->status) != 0 && *reinterpret_cast<volatile int *>(&hdr->site) != 0) return;
     atomicCAS(&hdr->status, 0, MINF_ERR_INVALID);
     atomicCAS(&hdr->site, 0, what | 0x20000000);
 }
@@ -64,32 +66,34 @@ __device__ __forceinline__ int page_of(const PagedSeqs &S, int s, int b, WsHeade
 }
 
 // Item `idx` of a call in which sequence s has count(s) items: its sequence and which
-// of that one's items it is.  The whole CTA calls it; false if there are fewer items.
+// of that one's items it is.  The whole CTA calls it; false if there are fewer items.  Sums are
+// 64-bit: starts that contradict each other can name the same rows over and over.
 template <int kThreads, class Count>
 __device__ __forceinline__ bool find_item(int n_seqs, int idx, Count count, int &seq, int &item) {
-    __shared__ int sums[kThreads / 32], hit[2];
+    __shared__ long long sums[kThreads / 32];
+    __shared__ int hit[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int per = (n_seqs + kThreads - 1) / kThreads;
     const int sa = min((int)threadIdx.x * per, n_seqs), sb = min(sa + per, n_seqs);
-    int mine = 0;
+    long long mine = 0;
     for (int s = sa; s < sb; ++s) mine += count(s);
-    int inc = mine;
+    long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
     }
     if (lane == 31) sums[warp] = inc;
     if (threadIdx.x == 0) hit[0] = -1;
     __syncthreads();
-    int at = inc - mine;
+    long long at = inc - mine;
     for (int w = 0; w < warp; ++w) at += sums[w];
     if (at <= idx && idx < at + mine) {
         for (int s = sa;; ++s) {
             const int n = count(s);
             if (idx < at + n) {
                 hit[0] = s;
-                hit[1] = idx - at;
+                hit[1] = (int)(idx - at);
                 break;
             }
             at += n;

@@ -138,7 +138,9 @@ __device__ __forceinline__ SeqCut seq_cut(const SeqView &v, int hkv, int tpt, co
 // partial slots are out.  If a single sequence has new tokens (a chunk of a long
 // prompt), its whole rounds of pairs may stay uncut and the rest alone be cut: 256
 // pairs of 448 tiles take 1,637 us cut into 4 each, 1,578 us with the last 108 cut.  Every
-// CTA computes the same result.
+// CTA computes the same result.  Starts that contradict each other can name the same rows
+// over and over; if they make more pairs than `total` rows can, none is worked on.
+constexpr int kNoPlan = 1 << 30;  // as a part length (no sequence is cut): no units
 struct PlanSum {
     long long units, cut;
     float work;
@@ -213,6 +215,12 @@ __device__ int choose_part_len(const ChunkParams &P, PlanSum (*sum)[32], int *le
         for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
         const unsigned at = __ballot_sync(0xffffffffu, cost <= best);
         if (lane == __ffs(at) - 1) *len_sh = code;
+        __syncwarp();
+        // lane 0 cuts nothing, its units are the pairs
+        if (lane == 0 && mine.units > P.a.hkv * (S.total / (2ll * P.tpt) + S.n_seqs)) {
+            flag_invalid(P.a.hdr, BAD_SEQ);
+            *len_sh = kNoPlan;
+        }
     }
     __syncthreads();
     return *len_sh;
@@ -322,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             return make_int2(c.units(), c.slots());
         };
         int2 mine = make_int2(0, 0);
-        for (int s = sa; s < sb; ++s) {
+        for (int s = sa; s < sb; ++s) {  // all of them fit 31 bits, or no unit is worked on
             const int2 c = count(s);
             mine.x += c.x;
             mine.y += c.y;
@@ -355,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int n_units = pre[S.n_seqs].x;
+    const int n_units = code == kNoPlan ? 0 : pre[S.n_seqs].x;
     if (blockIdx.x == 0 && warp == 3) {  // the joining kernel's copy: (slots, pairs) cut before each sequence
         int2 *dst = reinterpret_cast<int2 *>(P.a.plan + 1);
         int cut = 0;

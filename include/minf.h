@@ -285,7 +285,10 @@ int minf_mixed_layer(const minf_bf16 *q, const minf_bf16 *k, const minf_bf16 *v,
  *     outside [0, total) or kv_lens outside [0, width * page_size] is left out;
  *     a page number outside [0, num_pages) is left out by the append, and the
  *     keys concerned are unspecified in the others; MINF_ERR_INVALID is then
- *     recorded in the workspace's status word (minf_status).
+ *     recorded in the workspace's status word (minf_status).  Where the starts go
+ *     back, so that sequences name the same rows, the rows concerned are
+ *     unspecified; a chunk call whose sequences name more rows than there are does
+ *     nothing else than report it.
  *   - Sequences may have no new tokens.  Rows that belong to no sequence (behind
  *     cu_q[n_seqs]) are neither read nor written.
  *   - kv_lens[s] < n is allowed in all but the append: tokens whose position is

@@ -56,3 +56,40 @@ def test_workspace_serves_the_next_call_right_behind_a_selection(lens, pages):
         assert torch.equal(o, want[0]) and torch.equal(l, want[1])
         assert torch.equal(idx, wi) and torch.equal(cnt, wc)
     assert minf.minf_status(ws) == 0
+
+
+# ------------------------------------------------------------------ starts that name the same rows over and over
+def alternating(n_seqs, n):
+    """Every other sequence claims all n rows, the ones between end before they begin."""
+    return torch.tensor([0, n] * (n_seqs // 2) + [0], dtype=torch.int32, device="cuda")
+
+
+def test_append_counts_rows_named_over_and_over():
+    """2,048 sequences of 2^20 pages each: their sum passes 32 bits.  No table entry is a page."""
+    n_seqs, n = 4096, 1 << 24
+    k = torch.zeros(n * 8 + 128, dtype=BF, device="cuda").as_strided((n, 1, 128), (8, 128, 1))
+    kc = torch.zeros(2, 1, 16, 128, dtype=BF, device="cuda")
+    vc = torch.zeros_like(kc)
+    tables = torch.full((n_seqs, n // 16), -1, dtype=torch.int32, device="cuda")
+    kv = torch.full((n_seqs,), n, dtype=torch.int32, device="cuda")
+    ws = minf.workspace(minf.paged_workspace_bytes(minf.OP_PAGED_APPEND, 1, 1, n, n_seqs, n), "cuda")
+    minf.minf_paged_append(k, k, kc, vc, tables, alternating(n_seqs, n), kv, n, ws=ws)
+    assert minf.minf_status(ws) == minf.MINF_ERR_INVALID
+    assert (kc == 0).all() and (vc == 0).all()
+
+
+def test_chunk_works_on_no_rows_named_over_and_over():
+    """2,048 sequences that claim the same 4,096 tokens: more row tiles than the rows make."""
+    n_seqs, n = 4096, 4096
+    q = torch.zeros(n, 4, 128, dtype=BF, device="cuda")
+    kc = torch.zeros(256, 1, 16, 128, dtype=BF, device="cuda")
+    tables = torch.arange(256, dtype=torch.int32, device="cuda").expand(n_seqs, 256).contiguous()
+    kv = torch.full((n_seqs,), n, dtype=torch.int32, device="cuda")
+    ws = minf.workspace(minf.paged_workspace_bytes(minf.OP_PAGED_ATTENTION, 4, 1, n, n_seqs, n), "cuda")
+    out = torch.full_like(q, 7.0)
+    minf.minf_paged_attention(q, kc, kc, tables, alternating(n_seqs, n), kv, n, out=out, ws=ws)
+    assert minf.minf_status(ws) == minf.MINF_ERR_INVALID
+    assert (out == 7).all()
+    # the same workspace serves a call that makes sense
+    minf.minf_paged_attention(q, kc, kc, tables[:1], alternating(2, n)[:2], kv[:1], n, out=out, ws=ws)
+    assert minf.minf_status(ws) == 0 and (out == 0).all()

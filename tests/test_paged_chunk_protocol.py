@@ -226,3 +226,17 @@ def test_protocol_model_catches_faults(fault):
 def test_protocol_small_unit_lists(units):
     for seed in range(50):
         Model(units, seed).run()
+
+
+def test_rows_make_at_most_the_row_tile_pairs_that_the_plan_allows():
+    """Rising starts never exceed the limit above which the plan refuses to work: hkv (total / 2 tpt + n_seqs)."""
+    rng = random.Random(4)
+    for _ in range(2000):
+        tpt, hkv = rng.choice([1, 2, 3, 10, 32, 128]), rng.choice([1, 2, 8])
+        lens = [rng.choice([0, 1, rng.randrange(1, 600), 2 * tpt, 2 * tpt + 1]) for _ in range(rng.randrange(1, 30))]
+        pairs = hkv * sum(-(-n // (2 * tpt)) for n in lens)
+        assert pairs <= hkv * (sum(lens) // (2 * tpt) + len(lens))
+    # starts that name the same rows again pass it, and 32-bit sums of them would wrap
+    n, seqs, tpt = 1 << 24, 2048, 128
+    assert seqs * -(-n // (2 * tpt)) > n // (2 * tpt) + 2 * seqs
+    assert seqs * (n // 16) >= 1 << 31
