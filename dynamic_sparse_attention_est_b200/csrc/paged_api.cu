@@ -83,6 +83,10 @@ int check_seqs(const minf_paged_seqs *s, PagedSeqs &S, int hq) {
     return MINF_OK;
 }
 
+// Longest page list: no table names more pages (2^30 tokens in pages of 16), and its
+// entries times the 16-key groups of a page fit 31 bits.
+constexpr int kMaxTopk = 1 << 26;
+
 // [tokens][heads][128] rows: 16-byte rows and strides; written ones must not overlap.
 int check_rows(const minf_rows *r, const char *name, int total, int heads, bool written) {
     if (!r || !r->data) return bad(MINF_ERR_INVALID, "null %s", name);
@@ -231,7 +235,7 @@ size_t minf_paged_workspace_bytes(int op, int hq, int hkv, int total, int n_seqs
         if (topk < 1 || width < 1 || width > kMaxBlocks) return 0;
         return estimate_bytes(paged_estimate_plan(total, n_seqs, hkv, width), nullptr);
     case MINF_OP_PAGED_BLOCK_ATTENTION:
-        if (topk < 1) return 0;
+        if (topk < 1 || topk > kMaxTopk) return 0;
         return sparse_sizes(total, hkv, hq / hkv, topk, 128).total;  // the largest pages make the most shares
     }
     return 0;
@@ -365,6 +369,7 @@ int minf_paged_block_attention(const minf_paged_seqs *seqs, int dtype, int hq, i
     int rc = fill_attn(P, seqs, dtype, hq, hkv, d, q, cache, scale, out, lse);
     if (rc) return rc;
     if (topk < 1) return bad(MINF_ERR_INVALID, "topk must be >= 1");
+    if (topk > kMaxTopk) return bad(MINF_ERR_UNSUPPORTED, "topk=%d above %d", topk, kMaxTopk);
     const PagedSeqs &S = P.seqs;
     if (S.n_seqs == 0 || S.total == 0) return api_check_ws(ws, ws_bytes, MINF_STATUS_BYTES);
     if (!blk_idx || !blk_cnt) return bad(MINF_ERR_INVALID, "null blk_idx or blk_cnt");

@@ -385,7 +385,8 @@ int minf_paged_block_estimate(const minf_paged_seqs *seqs, int dtype, int hq, in
  * position p attends, for kv-head h, to the positions k <= p whose page k / P is
  * among blk_idx[t][h][0 .. blk_cnt[t][h]).  Lists must be ascending with distinct
  * entries (as minf_paged_block_estimate writes them); an entry that is negative,
- * past the token's own page or not above the one before it is left out.
+ * past the token's own page or not above the one before it is left out.  topk at
+ * most 2^26.
  */
 int minf_paged_block_attention(const minf_paged_seqs *seqs, int dtype, int hq, int hkv, int d,
                                const minf_rows *q, const minf_paged_cache *cache, float scale,

@@ -147,3 +147,13 @@ def test_binding_refuses_cpu_tensors_and_wrong_counts(minf_lib):
         minf.minf_paged_block_estimate(None, kc, t, cu, kv, 1)
     with pytest.raises(ValueError, match="arguments"):
         minf._paged().attention(q)
+
+
+def test_block_attention_refuses_lists_longer_than_a_table_can_name(minf_lib):
+    """2^26 pages of 16 tokens are all that a table names; longer lists would overflow the count of 16-key groups."""
+    most = 1 << 26
+    assert block_attention(topk=most + 1) == UNS and block_attention(topk=1 << 28) == UNS
+    assert block_attention(topk=most, wsb=256) == WS  # the limit itself only lacks its workspace here
+    f = minf.paged_workspace_bytes
+    assert f(minf.OP_PAGED_BLOCK_ATTENTION, 4, 2, 3, 2, 2, 8, most) > 0
+    assert f(minf.OP_PAGED_BLOCK_ATTENTION, 4, 2, 3, 2, 2, 8, most + 1) == 0
