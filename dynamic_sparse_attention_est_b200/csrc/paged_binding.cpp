@@ -134,6 +134,12 @@ int64_t integer(PyObject *o, const char *name) {
     return x;
 }
 
+bool truth(PyObject *o) {
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) throw python_error();  // the object's own exception
+    return x != 0;
+}
+
 // out (allocated unless given) and lse (allocated if wanted) of an attention call.
 struct Outputs {
     at::Tensor out, lse;
@@ -196,7 +202,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         rows = int32_of(t.size(0), "rope");
         rot = int32_of(t.size(1), "rope");
     }
-    const int interleaved = PyObject_IsTrue(a[9]);
+    const bool interleaved = truth(a[9]);
     void *bounds = nullptr;
     if (a[12] != Py_None) {
         const at::Tensor &t = tensor(a[12], "k_bounds");
@@ -230,7 +236,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const minf_rows rq = rows_of(q, "q", kind, total, hq);
     const double scale = a[7] == Py_None ? 1.0 / std::sqrt(128.0) : PyFloat_AsDouble(a[7]);
     if (PyErr_Occurred()) throw python_error();
-    const Outputs o = outputs_of(a[8], PyObject_IsTrue(a[9]), kind, total, hq);
+    const Outputs o = outputs_of(a[8], truth(a[9]), kind, total, hq);
     const size_t need = a[10] != Py_None ? 0
                                          : minf_paged_workspace_bytes(MINF_OP_PAGED_ATTENTION, (int)hq, (int)cache.hkv, seqs.total,
                                                                       seqs.n_seqs, seqs.max_q, seqs.width, 0);
@@ -298,7 +304,7 @@ PyObject *block_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int topk = int32_of(idx.size(2), "topk");
     const double scale = a[9] == Py_None ? 1.0 / std::sqrt(128.0) : PyFloat_AsDouble(a[9]);
     if (PyErr_Occurred()) throw python_error();
-    const Outputs o = outputs_of(a[10], PyObject_IsTrue(a[11]), kind, total, hq);
+    const Outputs o = outputs_of(a[10], truth(a[11]), kind, total, hq);
     const size_t need = a[12] != Py_None ? 0
                                          : minf_paged_workspace_bytes(MINF_OP_PAGED_BLOCK_ATTENTION, (int)hq, (int)cache.hkv,
                                                                       seqs.total, seqs.n_seqs, seqs.max_q, seqs.width, topk);

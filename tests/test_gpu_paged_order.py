@@ -93,3 +93,17 @@ def test_chunk_works_on_no_rows_named_over_and_over():
     # the same workspace serves a call that makes sense
     minf.minf_paged_attention(q, kc, kc, tables[:1], alternating(2, n)[:2], kv[:1], n, out=out, ws=ws)
     assert minf.minf_status(ws) == 0 and (out == 0).all()
+
+
+# ------------------------------------------------------------------ the binding
+def test_flags_without_a_truth_value_raise_their_own_error():
+    c = ref.Case([1], [20], 4, 2, 16, BF, seed=1)
+    no_truth = torch.zeros(2)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        minf.minf_paged_append(c.k_new, c.v_new, c.k_cache, c.v_cache, *c.meta(), interleaved=no_truth)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        minf.minf_paged_attention(c.q, c.k_cache, c.v_cache, *c.meta(), want_lse=no_truth)
+    with pytest.raises(ValueError, match="integer"):
+        minf.minf_paged_attention(c.q, c.k_cache, c.v_cache, c.tables, c.cu, c.kv_lens, "one")
+    with pytest.raises(TypeError):
+        minf.minf_paged_attention(c.q, c.k_cache, c.v_cache, *c.meta(), scale="a")
