@@ -9,7 +9,6 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
-#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/StringUtil.h>
 
@@ -113,11 +112,15 @@ Cache cache_of(PyObject *k_o, PyObject *v_o, const Kind &kind) {
     return x;
 }
 
-// The caller's workspace, or one of `need` zeroed bytes.
+// The caller's workspace, or one of `need` bytes of which the status block is zero: the
+// kernels write what they read of the rest (157 MB for a chunk).
 at::Tensor workspace_of(PyObject *o, size_t need, const Kind &k) {
-    if (o == Py_None)
-        return at::zeros({(int64_t)std::max(need, (size_t)MINF_STATUS_BYTES)},
-                         at::TensorOptions().dtype(at::kByte).device(k.dev));
+    if (o == Py_None) {
+        at::Tensor ws = at::empty({(int64_t)std::max(need, (size_t)MINF_STATUS_BYTES)},
+                                  at::TensorOptions().dtype(at::kByte).device(k.dev));
+        ws.narrow(0, 0, MINF_STATUS_BYTES).zero_();
+        return ws;
+    }
     const at::Tensor &ws = tensor(o, "ws");
     if (ws.scalar_type() != at::kByte || ws.device() != k.dev || !ws.is_contiguous())
         refuse("ws must be a contiguous uint8 tensor on ", k.dev);
