@@ -283,6 +283,8 @@ struct StreamPlan {
 };
 StreamPlan paged_stream_plan(int group, int max_q);
 StreamPlan paged_sparse_plan(int total, int hkv, int group, int topk, int page);
+// The largest plan of a call of at most so many tokens and list entries, for any page size.
+StreamPlan paged_sparse_reserve(int total, int hkv, int group, int topk);
 cudaError_t run_paged_stream(const PagedAttnParams &P, bool fp16, int rows, cudaStream_t st);
 cudaError_t run_paged_sparse(const PagedAttnParams &P, bool fp16, int rows, cudaStream_t st);
 
@@ -313,6 +315,8 @@ struct EstimatePlan {
     size_t n_scores, n_top;
 };
 EstimatePlan paged_estimate_plan(int total, int n_seqs, int hkv, int width);
+// Scores and tops that suffice for every call of at most so many tokens and table columns.
+EstimatePlan paged_estimate_reserve(int total, int hkv, int width);
 cudaError_t run_paged_estimate(const EstimateParams &P, bool fp16, cudaStream_t st);
 
 }  // namespace minf

@@ -145,10 +145,7 @@ AttnSizes dense_sizes(int n_seqs, int group, int max_q) {
     return attn_sizes(p.n_slots, p.part_rows, n_seqs + 2);
 }
 
-AttnSizes sparse_sizes(int total, int hkv, int group, int topk, int page) {
-    const StreamPlan p = paged_sparse_plan(total, hkv, group, topk, page);
-    return attn_sizes(p.n_slots, p.rows, 0);
-}
+AttnSizes sparse_sizes(const StreamPlan &p) { return attn_sizes(p.n_slots, p.rows, 0); }
 
 size_t estimate_bytes(const EstimatePlan &p, size_t *top_at) {
     const size_t a = round_up(MINF_STATUS_BYTES + p.n_scores * sizeof(float));
@@ -233,10 +230,10 @@ size_t minf_paged_workspace_bytes(int op, int hq, int hkv, int total, int n_seqs
         return dense_sizes(n_seqs, hq / hkv, max_q).total;
     case MINF_OP_PAGED_BLOCK_ESTIMATE:
         if (topk < 1 || width < 1 || width > kMaxBlocks) return 0;
-        return estimate_bytes(paged_estimate_plan(total, n_seqs, hkv, width), nullptr);
+        return estimate_bytes(paged_estimate_reserve(total, hkv, width), nullptr);
     case MINF_OP_PAGED_BLOCK_ATTENTION:
         if (topk < 1 || topk > kMaxTopk) return 0;
-        return sparse_sizes(total, hkv, hq / hkv, topk, 128).total;  // the largest pages make the most shares
+        return sparse_sizes(paged_sparse_reserve(total, hkv, hq / hkv, topk)).total;
     }
     return 0;
 }
@@ -373,10 +370,10 @@ int minf_paged_block_attention(const minf_paged_seqs *seqs, int dtype, int hq, i
     const PagedSeqs &S = P.seqs;
     if (S.n_seqs == 0 || S.total == 0) return api_check_ws(ws, ws_bytes, MINF_STATUS_BYTES);
     if (!blk_idx || !blk_cnt) return bad(MINF_ERR_INVALID, "null blk_idx or blk_cnt");
-    const AttnSizes z = sparse_sizes(S.total, hkv, P.group, topk, S.page);
+    const StreamPlan p = paged_sparse_plan(S.total, hkv, P.group, topk, S.page);
+    const AttnSizes z = sparse_sizes(p);
     if ((rc = api_check_ws(ws, ws_bytes, z.total))) return rc;
     place(P, z, ws);
-    const StreamPlan p = paged_sparse_plan(S.total, hkv, P.group, topk, S.page);
     P.blk_idx = blk_idx;
     P.blk_cnt = blk_cnt;
     P.topk = topk;

@@ -1117,17 +1117,40 @@ cudaError_t launch(EstimateParams P, cudaStream_t st) {
 
 }  // namespace
 
+static int score_stride(int width) { return (width + 3) & ~3; }
+
+// 64 MiB of scores at a time: written and read back inside L2
+constexpr long long kBatchScores = (64ll << 20) / 4;
+static int score_batch(int total, int hkv, int width) {
+    const long long row = (long long)score_stride(width) * hkv;
+    return (int)std::max<long long>(1, std::min<long long>(total, kBatchScores / row));
+}
+
+// Page ranges of a launch, of which launch_scores takes no more.
+constexpr int kRangePages = ScoreShape::kWarps * kStepPages;
+static long long score_ranges(int n_seqs, int hkv, int width) {
+    const long long most = (std::max(1, width - 1) + kRangePages - 1) / kRangePages;
+    return std::max<long long>(1, std::min<long long>({most, 296 / ((long long)n_seqs * hkv), kMaxRanges}));
+}
+
 EstimatePlan paged_estimate_plan(int total, int n_seqs, int hkv, int width) {
     EstimatePlan p{};
-    p.score_stride = (width + 3) & ~3;
-    // 64 MiB of scores at a time: written and read back inside L2
-    const long long row = (long long)p.score_stride * 4 * hkv;
-    p.batch = (int)std::max<long long>(1, std::min<long long>(total, (64ll << 20) / row));
+    p.score_stride = score_stride(width);
+    p.batch = score_batch(total, hkv, width);
     p.n_scores = (size_t)p.batch * hkv * p.score_stride;
-    // the ranges of a launch: see launch_scores
-    const long long most = (std::max(1, width - 1) + ScoreShape::kWarps * kStepPages - 1) / (ScoreShape::kWarps * kStepPages);
-    const long long ranges = std::max<long long>(1, std::min<long long>({most, 296 / ((long long)n_seqs * hkv), kMaxRanges}));
-    p.n_top = (size_t)(p.batch * hkv * ranges);
+    p.n_top = (size_t)p.batch * hkv * score_ranges(n_seqs, hkv, width);
+    return p;
+}
+
+EstimatePlan paged_estimate_reserve(int total, int hkv, int width) {
+    EstimatePlan p = paged_estimate_plan(total, 1, hkv, width);
+    // a narrower table's batch of more tokens may come closer to the 64 MiB
+    const long long row = (long long)p.score_stride * hkv;
+    p.n_scores = (size_t)std::min(total * row, std::max(kBatchScores, row));
+    // fewer sequences have more ranges; of the tables with r ranges, the narrowest has the
+    // largest batch
+    for (long long r = score_ranges(1, hkv, width); r >= 1; --r)
+        p.n_top = std::max(p.n_top, (size_t)(r * hkv * score_batch(total, hkv, (int)(r - 1) * kRangePages + (r > 1 ? 2 : 1))));
     return p;
 }
 

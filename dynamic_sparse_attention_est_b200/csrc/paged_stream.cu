@@ -786,6 +786,11 @@ cudaError_t stream_maps(StreamParams &SP, const PagedAttnParams &P, bool fp16) {
 
 StreamPlan paged_stream_plan(int group, int max_q) { return {max_q * group <= 8 ? 8 : 16, 2 * kStreamGrid}; }
 
+// CTAs that share the page lists of so many items.
+static long long sparse_shares(long long items, int topk, int page) {
+    return std::max(1ll, std::min<long long>({kStreamGrid, items * topk, items * topk * page / (4 * kGroup)}));
+}
+
 StreamPlan paged_sparse_plan(int total, int hkv, int group, int topk, int page) {
     const int rows = group <= 8 ? 8 : 16;
     const long long items = (long long)total * hkv * ((group + rows - 1) / rows);
@@ -793,8 +798,15 @@ StreamPlan paged_sparse_plan(int total, int hkv, int group, int topk, int page) 
     // tokens run side by side); below, equal shares of one wave, of four 16-key groups
     // at least.
     if (items >= 4 * kStreamGrid) return {rows, 0};
-    const long long shares = std::min<long long>({kStreamGrid, items * topk, items * topk * page / (4 * kGroup)});
-    return {rows, 2 * (int)std::max(1ll, shares)};
+    return {rows, 2 * (int)sparse_shares(items, topk, page)};
+}
+
+// Shares grow with the items, the lists and the pages, up to where a call has none; a call
+// of that size reserves what a smaller one of the same heads takes.
+StreamPlan paged_sparse_reserve(int total, int hkv, int group, int topk) {
+    const int rows = group <= 8 ? 8 : 16;
+    const long long items = (long long)total * hkv * ((group + rows - 1) / rows);
+    return {rows, 2 * (int)sparse_shares(items, topk, 128)};
 }
 
 cudaError_t run_paged_stream(const PagedAttnParams &P, bool fp16, int rows, cudaStream_t st) {

@@ -392,7 +392,8 @@ def _paged():
 
 def paged_workspace_bytes(op: int, hq: int, hkv: int, total: int, n_seqs: int, max_q_len: int, width: int = 0,
                           topk: int = 0) -> int:
-    """Workspace bytes of a paged call; width: columns of block_tables (estimate), topk: the block operations."""
+    """Workspace bytes of a paged call and of every smaller one of the same heads; width: columns of
+    block_tables (estimate), topk: the block operations."""
     return int(lib().minf_paged_workspace_bytes(op, hq, hkv, total, n_seqs, min(max_q_len, total), width, topk))
 
 

@@ -328,7 +328,10 @@ typedef struct {
 
 /*
  * Bytes of workspace of a paged call (MINF_OP_PAGED_*; topk for the two block
- * operations, width for the estimate).  0 for arguments the call would reject.
+ * operations, width for the estimate).  They suffice for every smaller call of the
+ * same operation and heads too (fewer tokens, sequences, new tokens of a sequence,
+ * table columns, list entries), so a buffer for the largest step serves them all.
+ * 0 for arguments the call would reject.
  */
 size_t minf_paged_workspace_bytes(int op, int hq, int hkv, int total, int n_seqs, int max_q, int width,
                                   int topk);

@@ -1,5 +1,6 @@
 """Refusals of the paged calls, on the host: through the C ABI before any CUDA call, and in the binding."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -157,3 +158,44 @@ def test_block_attention_refuses_lists_longer_than_a_table_can_name(minf_lib):
     f = minf.paged_workspace_bytes
     assert f(minf.OP_PAGED_BLOCK_ATTENTION, 4, 2, 3, 2, 2, 8, most) > 0
     assert f(minf.OP_PAGED_BLOCK_ATTENTION, 4, 2, 3, 2, 2, 8, most + 1) == 0
+
+
+def sizes(rng):
+    hkv = rng.choice([1, 2, 3, 8, 32, 128])
+    group = rng.choice([1, 2, 4, 7, 8, 9, 16, 33, 128])
+    total, width = int(2 ** rng.uniform(0, 14)), int(2 ** rng.uniform(0, 15))
+    return min(256 // hkv, group) * hkv, hkv, total, rng.randint(1, min(total, 4096)), rng.randint(1, total), width, rng.randint(1, 300)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_workspace_of_the_largest_step_serves_every_smaller_one(minf_lib, seed):
+    """Sizes do not fall with the tokens, sequences, new tokens, table columns or list entries of a step, and
+    a call takes a buffer that was sized for a larger one (past that check there is no device memory here)."""
+    rng = random.Random(seed)
+    f = minf.paged_workspace_bytes
+    steps = [(8, 32, 200, 200, 1, 2048, 100, [(147, 147, 1, 2048, 100), (1, 1, 1, 2048, 100), (20, 4, 1, 2048, 100)])]
+    for _ in range(300):
+        hq, hkv, total, n_seqs, max_q, width, topk = sizes(rng)
+        small = []
+        for _ in range(4):
+            t = rng.choice([total, rng.randint(1, total)])
+            q = rng.randint(1, min(max_q, t))
+            small.append((t, rng.randint(1, min(n_seqs, t)), q, rng.choice([width, rng.randint(1, width)]),
+                          rng.choice([topk, rng.randint(1, topk)])))
+        steps.append((hkv, hq, total, n_seqs, max_q, width, topk, small))
+    for hkv, hq, total, n_seqs, max_q, width, topk, small in steps:
+        for op in (minf.OP_PAGED_ATTENTION, minf.OP_PAGED_BLOCK_ESTIMATE, minf.OP_PAGED_BLOCK_ATTENTION):
+            have = f(op, hq, hkv, total, n_seqs, max_q, width, topk)
+            for t, n, q, w, k in small:
+                assert 0 < f(op, hq, hkv, t, n, q, w, k) <= have, (op, hq, hkv, total, t, n, q, w, k)
+                kw = dict(hq=hq, hkv=hkv, total=t, n_seqs=n, max_q=q, width=w, table_stride=w, wsb=have)
+                page = rng.choice([16, 32, 64, 128])
+                if op == minf.OP_PAGED_ATTENTION:
+                    rc = attention(page_size=page, q=rows(hq), out=rows(hq), c=cache(page, hkv), **kw)
+                elif op == minf.OP_PAGED_BLOCK_ESTIMATE:
+                    rc = estimate(page_size=page, q=rows(hq), topk=k, **kw)
+                else:
+                    s = seqs(page_size=page, **{x: kw[x] for x in ("total", "n_seqs", "max_q", "width", "table_stride")})
+                    rc = minf.lib().minf_paged_block_attention(ref(s), 0, hq, hkv, 128, ref(rows(hq)), ref(cache(page, hkv)),
+                                                               0.1, FAKE, FAKE, k, ref(rows(hq)), None, FAKE, have, None)
+                assert rc not in (0, WS, UNS), (op, rc, minf.lib().minf_last_error())
