@@ -51,8 +51,10 @@ def build_binding() -> str:
     for d in inc:
         cmd += ["-isystem" if d != INCLUDE else "-I", d]
     lib = os.path.join(root, "lib")
-    cmd += [os.path.join(CSRC, "paged_binding.cpp"), LIB, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
-            "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    # by name, not path: the module finds the library beside itself (which carries no soname, so
+    # that programs linked by its path load it from there)
+    cmd += [os.path.join(CSRC, "paged_binding.cpp"), "-L", PKG, "-l:libminf.so", "-L", lib, "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     subprocess.check_call(cmd)
     os.replace(tmp, BINDING)
     return BINDING
@@ -94,8 +96,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if failed:
         raise RuntimeError(f"nvcc failed for {failed}")
     tmp = f"{LIB}.{os.getpid()}.tmp"
-    link = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-Xlinker", "-soname=libminf.so", "-o", tmp,
-            *objs]
+    link = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]
     subprocess.check_call(link)
     os.replace(tmp, LIB)
     build_binding()
