@@ -1,5 +1,7 @@
 """Builds libminf.so (the sm_100a kernels and the C ABI) in-tree with nvcc, and
-_paged.so (the torch binding of the paged calls) with g++.
+beside it, with g++, the torch binding of the paged calls.  The
+library needs neither torch nor Python's headers: where they are missing it is
+built all the same, and the build warns that the binding is not.
 
     python -m dynamic_sparse_attention_est_b200.build_lib [--force]
 """
@@ -7,15 +9,17 @@ from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libminf.so")
-BINDING = os.path.join(PKG, "_paged.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -36,17 +40,41 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def build_binding() -> str:
-    """Compiles the extension module against this interpreter's torch and links it to libminf.so."""
-    import sysconfig
+def cuda_include() -> str:
+    """The CUDA headers of the toolkit that nvcc() belongs to."""
+    found = shutil.which(nvcc())
+    roots = [os.path.dirname(os.path.dirname(os.path.abspath(found)))] if found else []
+    if found:
+        roots.append(os.path.dirname(os.path.dirname(os.path.realpath(found))))
+    roots += [os.environ.get("CUDA_HOME"), "/usr/local/cuda"]
+    for root in roots:
+        if root and os.path.exists(os.path.join(root, "include", "cuda_runtime_api.h")):
+            return os.path.join(root, "include")
+    raise RuntimeError("no CUDA headers beside nvcc, in CUDA_HOME or in /usr/local/cuda")
 
+
+def cxx() -> str:
+    """The system's compiler.  Not CXX: one that links a C++ runtime of its own into the module builds it
+    without complaint, and the first exception it throws through torch's ends the process."""
+    return "g++"
+
+
+def binding_path() -> str:
+    """The binding for this Python and this torch: another of either is another file."""
     import torch
 
-    root = os.path.dirname(torch.__file__)
+    return os.path.join(PKG, f"_paged.{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}.so")
+
+
+def build_binding() -> str:
+    """Compiles the extension module against this interpreter's torch and links it to libminf.so."""
+    import torch
+
+    path, root = binding_path(), os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           "/usr/local/cuda/include", sysconfig.get_paths()["include"], INCLUDE]
-    tmp = f"{BINDING}.{os.getpid()}.tmp"
-    cmd = ["g++", "-O2", "-fPIC", "-std=c++17", "-shared", "-o", tmp,
+           cuda_include(), sysconfig.get_paths()["include"], INCLUDE]
+    tmp = f"{path}.{os.getpid()}.tmp"
+    cmd = [cxx(), "-O2", "-fPIC", "-std=c++17", "-shared", "-o", tmp,
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     for d in inc:
         cmd += ["-isystem" if d != INCLUDE else "-I", d]
@@ -56,23 +84,36 @@ def build_binding() -> str:
     cmd += [os.path.join(CSRC, "paged_binding.cpp"), "-L", PKG, "-l:libminf.so", "-L", lib, "-lc10", "-lc10_cuda",
             "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     subprocess.check_call(cmd)
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, path)
+    return path
+
+
+def _older(path: str, deps) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path) for p in deps)
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-    deps += glob.glob(os.path.join(INCLUDE, "*.h")) + glob.glob(os.path.join(CSRC, "*.cpp"))
-    return any(os.path.getmtime(p) > t for p in deps)
+    return _older(LIB, deps + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _binding_stale() -> bool:
+    return _older(binding_path(), glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compiles every .cu under csrc/ into one shared library, and the binding; returns the library's path."""
-    if not force and not _stale():
-        return LIB
+    if force or _stale():
+        _build_library(verbose, ptxas_info)
+    try:
+        if force or _binding_stale():
+            build_binding()
+    except (ImportError, OSError, RuntimeError, subprocess.CalledProcessError) as e:
+        warnings.warn(f"{LIB} is built; the torch binding of the paged calls is not: {e}")
+    return LIB
+
+
+def _build_library(verbose: bool, ptxas_info: bool) -> None:
     build_dir = os.path.join(PKG, "_build")
     os.makedirs(build_dir, exist_ok=True)
     objs = []
@@ -99,8 +140,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     link = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]
     subprocess.check_call(link)
     os.replace(tmp, LIB)
-    build_binding()
-    return LIB
 
 
 def ensure_built() -> str:

@@ -10,11 +10,14 @@ raised.  See ``include/minf.h`` for the semantics of each call.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 from typing import Dict, Optional, Sequence, Tuple
 
 import torch
+
+from . import build_lib
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libminf.so")
@@ -384,8 +387,13 @@ def _paged():
     global _paged_module
     if _paged_module is None:
         lib()
-        from . import _paged as module  # built with libminf.so
-
+        path = build_lib.binding_path()
+        if not os.path.exists(path):
+            raise ImportError(f"{path}, the binding for this Python and torch, is not built: run python -m "
+                              "dynamic_sparse_attention_est_b200.build_lib")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._paged", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
         _paged_module = module
     return _paged_module
 
