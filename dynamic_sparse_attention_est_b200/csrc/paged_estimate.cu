@@ -24,11 +24,14 @@
 //           approximate score t by counting over a shrinking range of its key bits
 //           until few keys are left, which are ranked; then every page within 2 E of
 //           t is scored again in 64 bits; all others are decided by the
-//           approximation.  So the selection is that of exact scores.
+//           approximation.  So the selection is that of 64-bit scores (which decide
+//           ties to their own rounding: pages of equal bounds score alike to the bit).
 // E = (2^-15 + G 2^-23) |Q|_1 max|bound|: the two-part split of bf16 loses 2^-16
-// (fp16's less), sixteen accumulation steps at 2^-22 of the magnitudes each lose
-// 2^-18, the sums Q lose G 2^-24; 1.6 times their sum, since the instruction's
-// rounding is not documented.
+// (fp16's less), the sums Q lose G 2^-24, and sixteen accumulation steps are taken to
+// lose 2^-18, 2^-22 of the magnitudes each; 1.6 times their sum.  The last of the three
+// is an assumption, since the instruction's rounding is not documented; scores made to
+// cancel, to round one way or to drop their last bits come to 0.08 E at most, with
+// either score kernel and either type.
 #include <algorithm>
 
 #include "internal.h"

@@ -375,7 +375,7 @@ int minf_paged_attention(const minf_paged_seqs *seqs, int dtype, int hq, int hkv
  *         max(q[g][c] * min[j][c], q[g][c] * max[j][c]),
  * an upper bound of the group's summed q . k of any key in the page.  The
  * token's own page p / P is always kept; the best topk - 1 earlier pages join it,
- * by exact score (ties to the lower page).  Output, ASCENDING, -1 padded:
+ * by their scores in 64 bits (ties to the lower page).  Output, ASCENDING, -1 padded:
  *   blk_idx int32 [total][hkv][topk], blk_cnt int32 [total][hkv].
  * width at most 32768.
  */
