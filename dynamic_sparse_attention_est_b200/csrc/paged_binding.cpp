@@ -64,7 +64,7 @@ minf_paged_seqs seqs_of(PyObject *tables_o, PyObject *cu_o, PyObject *kv_o, int6
     const at::Tensor &tables = tensor(tables_o, "block_tables"), &cu = tensor(cu_o, "cu_q"),
                      &kv = tensor(kv_o, "kv_lens");
     auto check = [&](const at::Tensor &t, const char *name, int64_t nd) {
-        if (t.scalar_type() != at::kInt || t.device() != k.dev || t.dim() != nd || (t.numel() && t.stride(nd - 1) != 1))
+        if (t.scalar_type() != at::kInt || t.device() != k.dev || t.dim() != nd || (t.size(nd - 1) > 1 && t.stride(nd - 1) != 1))
             refuse(name, " must be a ", nd, "-D int32 tensor on ", k.dev, " with a contiguous last dimension");
     };
     check(tables, "block_tables", 2);
