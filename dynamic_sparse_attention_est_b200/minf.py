@@ -379,6 +379,11 @@ def minf_mixed_layer(q, k, v, head_patterns: Sequence[str], last_q: int = 64, n_
 
 
 # ---------------------------------------------------------------- paged cache
+# Lengths, pages, positions and lists lie on the device and are checked there: what is
+# wrong is left out, its rows of a new output are whatever memory held, and only
+# minf_status(ws) tells of it.  A call with ws=None gives its workspace back with the
+# status word unread, so a program that cannot vouch for its arrays passes a ws (one
+# for all four calls, in turn) and reads the status where it synchronises anyway.
 _paged_module = None
 
 
@@ -409,7 +414,8 @@ def minf_paged_append(k, v, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q
                       interleaved: bool = False, q=None, q_out=None, k_bounds=None, ws=None):
     """Stores the new tokens' keys (rotated with `rope`, fp32 [positions, rot]) and values in the paged cache,
     updates `k_bounds` [pages, hkv, 2, 128], and returns the rotated queries (q_out, allocated if None; None
-    without q).  q, k, v: [tokens, heads, 128], any strides over tokens and heads."""
+    without q).  q, k, v: [tokens, heads, 128], any strides over tokens and heads.  Faults that the device finds
+    in the arrays are seen only by minf_status(ws), with a ws of the caller's."""
     rc, out, _ = _paged().append(k, v, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q_len, rope, interleaved, q,
                                  q_out, k_bounds, ws)
     if rc:
@@ -419,7 +425,8 @@ def minf_paged_append(k, v, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q
 
 def minf_paged_attention(q, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q_len: int,
                          scale: Optional[float] = None, out=None, want_lse: bool = True, ws=None):
-    """Causal attention of the new tokens q [tokens, hq, 128] over everything stored; (out, lse [tokens, hq])."""
+    """Causal attention of the new tokens q [tokens, hq, 128] over everything stored; (out, lse [tokens, hq]).
+    Faults that the device finds in the arrays are seen only by minf_status(ws), with a ws of the caller's."""
     rc, out, lse = _paged().attention(q, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q_len, scale, out, want_lse,
                                       ws)
     if rc:
@@ -429,7 +436,8 @@ def minf_paged_attention(q, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q
 
 def minf_paged_block_estimate(q, k_bounds, block_tables, cu_q, kv_lens, max_q_len: int, page_size: int = 64,
                               topk: int = 100, ws=None):
-    """Pages selected for every new token and kv-head: (blk_idx [tokens, hkv, topk], blk_cnt [tokens, hkv])."""
+    """Pages selected for every new token and kv-head: (blk_idx [tokens, hkv, topk], blk_cnt [tokens, hkv]).
+    Faults that the device finds in the arrays are seen only by minf_status(ws), with a ws of the caller's."""
     rc, idx, cnt = _paged().block_estimate(q, k_bounds, block_tables, cu_q, kv_lens, max_q_len, page_size, topk, ws)
     if rc:
         _check(rc, "minf_paged_block_estimate")
@@ -438,7 +446,8 @@ def minf_paged_block_estimate(q, k_bounds, block_tables, cu_q, kv_lens, max_q_le
 
 def minf_paged_block_attention(q, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q_len: int, blk_idx, blk_cnt,
                                scale: Optional[float] = None, out=None, want_lse: bool = True, ws=None):
-    """Causal attention of every new token over its listed pages only; (out, lse [tokens, hq])."""
+    """Causal attention of every new token over its listed pages only; (out, lse [tokens, hq]).
+    Faults that the device finds in the arrays are seen only by minf_status(ws), with a ws of the caller's."""
     rc, out, lse = _paged().block_attention(q, k_cache, v_cache, block_tables, cu_q, kv_lens, max_q_len, blk_idx, blk_cnt,
                                             scale, out, want_lse, ws)
     if rc:

@@ -297,7 +297,9 @@ int minf_mixed_layer(const minf_bf16 *q, const minf_bf16 *k, const minf_bf16 *v,
  *     included.  Keys and values of stored positions must be finite.
  *   - The workspace is as everywhere: at least minf_paged_workspace_bytes, its
  *     first MINF_STATUS_BYTES zero before its first use, used by one call at a
- *     time (also by one captured graph's replay at a time).
+ *     time (also by one captured graph's replay at a time).  Faults that only the
+ *     device can see are reported there alone: the call itself returns MINF_OK,
+ *     and the rows of what was left out keep what they held.
  *   - The caller's current device is left as it was.
  */
 #define MINF_BF16 0

@@ -26,3 +26,20 @@ def test_one_element_arrays_may_have_any_stride():
     assert apart[::4].stride(0) == 4 and torch.equal(got, want[:1])
     with pytest.raises(ValueError, match="contiguous last"):
         minf.minf_paged_attention(c.q, c.k_cache, c.v_cache, c.tables, c.cu, apart[::3], 1, scale=SCALE)
+
+
+def test_a_fault_in_a_call_without_a_workspace_goes_unreported_and_no_further():
+    """The call returns, the rows left out keep what they held, and the next call finds no trace of it; with
+    a workspace the same call is reported."""
+    c = ref.Case([1, 1], [300, 90], 4, 2, 64, BF, seed=2)
+    want, _ = minf.minf_paged_attention(c.q, c.k_cache, c.v_cache, *c.meta(), scale=SCALE)
+    bad = c.kv_lens.clone()
+    bad[1] = -1
+    out = torch.full((2, 4, 128), 9.0, dtype=BF, device="cuda")
+    minf.minf_paged_attention(c.q, c.k_cache, c.v_cache, c.tables, c.cu, bad, 1, scale=SCALE, out=out)
+    assert torch.equal(out[0], want[0]) and (out[1] == 9).all()
+    ws = minf.workspace(minf.paged_workspace_bytes(minf.OP_PAGED_ATTENTION, 4, 2, 2, 2, 1), "cuda")
+    got, _ = minf.minf_paged_attention(c.q, c.k_cache, c.v_cache, *c.meta(), scale=SCALE, ws=ws)
+    assert torch.equal(got, want) and minf.minf_status(ws) == 0
+    minf.minf_paged_attention(c.q, c.k_cache, c.v_cache, c.tables, c.cu, bad, 1, scale=SCALE, out=out, ws=ws)
+    assert minf.minf_status(ws) == minf.MINF_ERR_INVALID
