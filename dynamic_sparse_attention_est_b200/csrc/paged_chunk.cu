@@ -29,6 +29,10 @@
 // by every CTA alike from the lengths on the device so that the units fill the SMs
 // in whole rounds; units that run side by side share their kv-head and key range,
 // which keeps K and V in L2.  Parts of a cut pair are joined by a second kernel.
+//
+// O grows in TMEM by the tensor cores' fp32 additions, which truncate: over one page
+// repeated, uncut, it comes out low by 1.1e-4 of the value after 128K keys and by
+// 9.0e-4 after 1M, in either type.
 #include <cstring>
 
 #include "internal.h"

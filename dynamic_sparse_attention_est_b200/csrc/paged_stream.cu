@@ -22,7 +22,8 @@
 //     wherever in an item a share ends: the 16-key groups of all sequences (each CTA
 //     takes the prefix sums of the lengths itself, so that a captured launch follows
 //     them), or the entries of all page lists.  An item's parts are joined by a second
-//     small kernel in a fixed order.
+//     small kernel in a fixed order.  Lists are cut as if they were topk long: where they
+//     are far shorter, the CTAs whose shares lie behind the counts have nothing to do.
 #include <algorithm>
 #include <cstring>
 
@@ -40,7 +41,9 @@ constexpr uint32_t kBoxBytes = 2048;             // 16 keys x 64 channels
 constexpr uint32_t kStageBytes = 4 * kBoxBytes;  // K low, K high, V low, V high channels
 constexpr uint32_t kRingBytes = 12 * kStageBytes;
 constexpr uint32_t kSmemBar = kRingBytes;         // mbarriers, abort flag
-constexpr uint32_t kSmemPre = kSmemBar + 256;     // [n_seqs + 1] units before a sequence (dense)
+// [n_seqs + 1] units before a sequence (dense): beside the rings there is room for two CTAs
+// on an SM up to 2,015 sequences; from there on the shares run in two waves
+constexpr uint32_t kSmemPre = kSmemBar + 256;
 
 // Warps of a CTA and groups in flight to each, by the registers that NT row tiles
 // take: six warps of two with one tile (313 tokens with 64 pages of 32: 64.6 us; four of
