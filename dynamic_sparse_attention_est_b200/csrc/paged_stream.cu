@@ -201,7 +201,12 @@ __device__ __forceinline__ void step(State<Ty, NT> &st, uint32_t stage, const ui
             st.l[t][i] += p[i] + p[2 + i];
         }
         // P is rounded to the cache's type for the product (half a step, 2^-8 of a
-        // bf16 weight: the size of the output's own rounding); the sum keeps fp32
+        // bf16 weight: the size of the output's own rounding); the sum keeps fp32.  P in
+        // two parts leaves the output's rounding alone (error against 64 bits 0.0017 of
+        // the norm instead of 0.0023 in bf16, 0.00021 instead of 0.00029 in fp16) and
+        // takes 1 % longer on 64 sequences of up to 32K tokens, 7 % on one sequence's 100
+        // pages, 5 to 8 % on chunks over their pages: not worth it beside the prompt's
+        // kernels, which round alike.
         pb[t][0] = transpose8x8(Ty::pack(p[0], p[1]));
         pb[t][1] = transpose8x8(Ty::pack(p[2], p[3]));
     }
